@@ -221,6 +221,52 @@ paro_status paro_linear_partial(const paro_rot* rot, const void* X_dev,
 paro_status paro_finalize(const float* Yf_dev, const void* bias_dev, void* Y_dev, int64_t tokens,
                           int64_t out_features, paro_stream stream);
 
+/* Root-mean-square norm between the layers, with the residual's addition:
+ *     v = x + b + r            (fp32; b and r optional)
+ *     H = fp16(v)              (the residual stream for the next addition)
+ *     Y = fp16(v weight / sqrt(mean(v^2) + eps))
+ * The mean is over the row's `features` channels, in fp32 of the unrounded v,
+ * and Y is rounded once. (No counterpart in the paper: it is what a decoder
+ * block computes between two of its rotated layers.)
+ *   X_dev         [tokens][features] fp16 (x_fp32 = 0), or fp32 (x_fp32 = 1):
+ *                 the summed shares of a row-parallel layer, which then need
+ *                 no paro_finalize
+ *   residual_dev  r, fp16 [tokens][features] or NULL
+ *   bias_dev      b, fp16 [features] or NULL (the row-parallel layer's bias)
+ *   weight_dev    fp16 [features];  eps > 0
+ *   H_dev         fp16 [tokens][features] or NULL (not wanted)
+ *   Y_dev         fp16 [tokens][features]
+ *   features      a positive multiple of 16, at most 32768; tokens >= 0
+ * H or Y may be exactly X (fp16) or residual (in place); other overlaps are
+ * PARO_ERR_ARG. Every pointer is 16-byte aligned. A row's result does not
+ * depend on the other rows. Values follow IEEE arithmetic: a NaN or infinity
+ * in a row makes its norm NaN where v is NaN or infinite, and 0 elsewhere for
+ * an infinity, NaN everywhere for a NaN. */
+paro_status paro_rmsnorm(const void* X_dev, int x_fp32, const void* residual_dev, const void* bias_dev,
+                         const void* weight_dev, float eps, void* H_dev, void* Y_dev, int64_t tokens,
+                         int64_t features, paro_stream stream);
+
+/* paro_rmsnorm with its output in 8 bits: with y the unrounded fp32 norm,
+ *     Q = e4m3(y / s),   s = max|y| / 448
+ * rounded to nearest even, s over each 128 channels of a row (the last group
+ * of a row may be shorter) for scale_group = 128, or over the row for
+ * scale_group = 0 (others: PARO_ERR_UNSUPPORTED). s is floored at 2^-100 (an
+ * all-zero group has zero codes); a NaN y gets the NaN code and does not
+ * enter s. Half the bytes of fp16, for a hidden state that has to cross
+ * between GPUs before a layer reads it; paro_q8_expand restores fp16.
+ *   Q_dev         e4m3 bytes [tokens][features]
+ *   scales_dev    fp32 [tokens][ceil(features / 128)], or [tokens]
+ * Other arguments and errors as paro_rmsnorm (Q and scales may not overlap
+ * any input). */
+paro_status paro_rmsnorm_q8(const void* X_dev, int x_fp32, const void* residual_dev, const void* bias_dev,
+                            const void* weight_dev, float eps, int scale_group, void* H_dev, void* Q_dev,
+                            float* scales_dev, int64_t tokens, int64_t features, paro_stream stream);
+
+/* Y = fp16(Q s): the codes and scales of paro_rmsnorm_q8 back to fp16
+ * [tokens][features], with one rounding. Arguments as there. */
+paro_status paro_q8_expand(const void* Q_dev, const float* scales_dev, int scale_group, void* Y_dev,
+                           int64_t tokens, int64_t features, paro_stream stream);
+
 /* paro_linear for decode batches (tokens <= 16) that allocates nothing and
  * takes no workspace: for callers that cannot allocate device memory, such
  * as a serving engine that hands all device memory to its own pool at start-

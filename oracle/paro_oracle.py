@@ -192,6 +192,50 @@ def linear_fp16_pipeline(x: np.ndarray, pairs, theta, alpha, q, s, z, group: int
 
 
 # --------------------------------------------------------------------------
+# The decoder block around the layer: epilogues, gated product, norm
+# --------------------------------------------------------------------------
+def activation(v: np.ndarray, act: str) -> np.ndarray:
+    """none, relu, silu v / (1 + e^-v), gelu v Phi(v), or gelu_tanh
+    v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))."""
+    v = np.asarray(v, dtype=np.float64)
+    if act == "none":
+        return v
+    if act == "relu":
+        return np.where(v < 0, 0.0, v)          # a NaN stays a NaN
+    if act == "silu":
+        with np.errstate(over="ignore"):
+            return v / (1.0 + np.exp(-v))
+    if act == "gelu":
+        from math import erfc, sqrt
+        return v * 0.5 * np.vectorize(erfc, otypes=[np.float64])(-v / sqrt(2.0))
+    if act == "gelu_tanh":
+        return 0.5 * v * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3)))
+    raise ValueError(act)
+
+
+def rmsnorm(x, weight, eps, residual=None, bias=None):
+    """(v, y) in fp64: v = x + bias + residual, y = v weight / sqrt(mean(v^2) + eps) per row."""
+    v = np.asarray(x, dtype=np.float64)
+    if bias is not None:
+        v = v + np.asarray(bias, dtype=np.float64)[None, :]
+    if residual is not None:
+        v = v + np.asarray(residual, dtype=np.float64)
+    r = 1.0 / np.sqrt(np.mean(v * v, axis=1, keepdims=True) + eps)
+    return v, v * r * np.asarray(weight, dtype=np.float64)[None, :]
+
+
+def q8_scales(y: np.ndarray, scale_group: int) -> np.ndarray:
+    """max|y| / 448 per 128 channels (the last group of a row may be shorter)
+    or per row (scale_group 0), floored at 2^-100."""
+    y = np.abs(np.asarray(y, dtype=np.float64))
+    T, F = y.shape
+    c = 128 if scale_group else F
+    n = -(-F // c)
+    m = np.concatenate([y, np.zeros((T, n * c - F))], axis=1).reshape(T, n, c).max(axis=2)
+    return np.maximum(m / 448.0, 2.0 ** -100)
+
+
+# --------------------------------------------------------------------------
 # Error measures used by the parity tests
 # --------------------------------------------------------------------------
 def rotation_rel_error(got: np.ndarray, ref: np.ndarray, group: int = GROUP, floor: float = 1e-2):

@@ -8,6 +8,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -23,7 +24,7 @@ _STATUS = {0: "PARO_OK", 1: "PARO_ERR_ARG", 2: "PARO_ERR_UNSUPPORTED", 3: "PARO_
 
 _lib: Optional[ctypes.CDLL] = None
 
-_vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_vp, _i64, _int, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "paro_rot_create": [ctypes.POINTER(_vp), _i64, _int, _int, _int, _vp, _vp, _vp],
     "paro_rot_destroy": [_vp],
@@ -42,6 +43,9 @@ _SIGS = {
     "paro_linear_ex": [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "paro_linear_partial": [_vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "paro_finalize": [_vp, _vp, _vp, _i64, _i64, _vp],
+    "paro_rmsnorm": [_vp, _int, _vp, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _vp],
+    "paro_rmsnorm_q8": [_vp, _int, _vp, _vp, _vp, _f32, _int, _vp, _vp, _vp, _i64, _i64, _vp],
+    "paro_q8_expand": [_vp, _vp, _int, _vp, _i64, _i64, _vp],
     "paro_rotate_once": [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _int, _int, _int, _vp],
     "paro_linear_once": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp],
     "paro_fault_status": [ctypes.POINTER(_int), _int],
@@ -89,6 +93,18 @@ def _stream(stream, device: Optional[torch.device] = None) -> int:
             return int(_raw_stream(idx))
         stream = torch.cuda.current_stream(idx)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Context in which `device` is current: entering it costs nothing when it
+    already is (a kernel launches on the current device's stream)."""
+    if _current_device is not None and _current_device() == device.index:
+        return _HERE
+    return torch.cuda.device(device)
 
 
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
@@ -413,4 +429,89 @@ def paro_linear_noalloc(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
         rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"),
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _stream(stream, X.device)))
+    return Y
+
+
+def _f16(t: torch.Tensor, shape, device: int, name: str) -> int:
+    """Data pointer of a contiguous fp16 tensor of this shape on CUDA device `device`."""
+    if t.dtype is not torch.float16 or not t.is_cuda or not t.is_contiguous():
+        _dev(t, torch.float16, name)                        # says which of the three it is
+    if t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be {list(shape)} on cuda:{device}, got {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _norm_args(X, weight, residual, bias, H):
+    """Shape, pointers and H of a norm after the checks its two forms share; H
+    is allocated when a residual, a bias or fp32 sums make it differ from X."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in (torch.float16, torch.float32):
+        raise TypeError("X must be a [tokens][features] fp16 or fp32 CUDA tensor")
+    x = _dev(X, X.dtype, "X")
+    x32 = X.dtype is torch.float32
+    shape, dev = X.shape, X.get_device()
+    row = shape[1:]
+    if H is None and (residual is not None or bias is not None or x32):
+        H = torch.empty(shape, dtype=torch.float16, device=X.device)
+    return shape, (x, int(x32),
+                   None if residual is None else _f16(residual, shape, dev, "residual"),
+                   None if bias is None else _f16(bias, row, dev, "bias"),
+                   _f16(weight, row, dev, "weight")), \
+        None if H is None else _f16(H, shape, dev, "H"), H
+
+
+def _out(t, shape, dtype, device, name):
+    """An output: allocated, or the given tensor after its checks."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dev(t, dtype, name)
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {list(shape)} on {device}, got {list(t.shape)} on {t.device}")
+    return t
+
+
+def paro_rmsnorm(X: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, H: Optional[torch.Tensor] = None,
+                 Y: Optional[torch.Tensor] = None, stream=None):
+    """(Y, H): v = X + bias + residual, H = fp16(v), Y = fp16 of v's
+    root-mean-square norm times weight. X fp16, or fp32 sums of a row-parallel
+    layer. H is None when nothing is added to an fp16 X and no H is given;
+    H=residual updates the residual stream in place."""
+    shape, args, h, H = _norm_args(X, weight, residual, bias, H)
+    if Y is None:
+        Y = torch.empty(shape, dtype=torch.float16, device=X.device)
+    y = _f16(Y, shape, X.get_device(), "Y")
+    with _on(X.device):
+        st = lib().paro_rmsnorm(*args, eps, h, y, *shape, _stream(stream, X.device))
+    if st != PARO_OK:
+        _check("paro_rmsnorm", st)
+    return Y, H
+
+
+def paro_rmsnorm_q8(X: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, scale_group: int = 128, H: Optional[torch.Tensor] = None,
+                    Y: Optional[torch.Tensor] = None, S: Optional[torch.Tensor] = None, stream=None):
+    """(codes, scales, H): paro_rmsnorm with Y as float8_e4m3fn codes and fp32
+    scales [tokens][ceil(features / 128)] (scale_group 128) or [tokens][1]
+    (scale_group 0: one scale per row)."""
+    shape, args, h, H = _norm_args(X, weight, residual, bias, H)
+    T, F = shape
+    Y = _out(Y, shape, torch.float8_e4m3fn, X.device, "Y")
+    S = _out(S, (T, -(-F // 128) if scale_group else 1), torch.float32, X.device, "S")
+    with _on(X.device):
+        _check("paro_rmsnorm_q8", lib().paro_rmsnorm_q8(*args, eps, scale_group, h, Y.data_ptr(), S.data_ptr(), T, F,
+                                                        _stream(stream, X.device)))
+    return Y, S, H
+
+
+def paro_q8_expand(Q: torch.Tensor, S: torch.Tensor, scale_group: int = 128, Y: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """fp16(code * scale) of paro_rmsnorm_q8's codes and scales."""
+    q, s = _dev(Q, torch.float8_e4m3fn, "Q"), _dev(S, torch.float32, "S")
+    if Q.dim() != 2 or S.shape != (Q.shape[0], -(-Q.shape[1] // 128) if scale_group else 1) or S.device != Q.device:
+        raise ValueError("S must hold one scale per row, or per 128 channels of a row, of Q [tokens][features]")
+    T, F = Q.shape
+    Y = _out(Y, (T, F), torch.float16, Q.device, "Y")
+    with _on(Q.device):
+        _check("paro_q8_expand", lib().paro_q8_expand(q, s, scale_group, Y.data_ptr(), T, F,
+                                                      _stream(stream, Q.device)))
     return Y

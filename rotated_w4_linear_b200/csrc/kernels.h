@@ -75,6 +75,15 @@ cudaError_t launch_gemm(const void* Xr, const void* qw, const void* scp, const v
 // row-parallel layer after the partial sums were added across ranks.
 cudaError_t launch_finalize(const float* Yf, const void* bias, void* Y, int64_t T, int64_t out, cudaStream_t s);
 
+// v = x + b + r, H = fp16(v), Y = norm(v) in fp16, or (S not null) e4m3 codes
+// with one scale per 128 channels (scale_group != 0) or per row. x fp16 or
+// fp32; r, b, H may be null; H may be x or r.
+cudaError_t launch_rmsnorm(const void* x, bool x_fp32, const void* r, const void* b, const void* w, float eps, void* H,
+                           void* Y, float* S, int scale_group, int64_t T, int64_t F, cudaStream_t s);
+// Y = fp16(code * scale)
+cudaError_t launch_q8_expand(const void* Q, const float* S, int scale_group, void* Y, int64_t T, int64_t F,
+                             cudaStream_t s);
+
 // A kernel whose bounded wait runs out on purpose after limit_ns (fault code 6).
 cudaError_t launch_wait_selftest(uint64_t limit_ns, cudaStream_t s);
 

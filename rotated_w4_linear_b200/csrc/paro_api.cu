@@ -36,6 +36,12 @@ paro_status cuda_fail(cudaError_t e, const char* what) {
     return fail(PARO_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The kernels are built for sm_100a only; refuse anything else up front.
@@ -705,6 +711,86 @@ paro_status paro_linear_once(const void* X, const int16_t* pairs, const float* t
     if (ws) cudaFree(ws);
     const paro_status st2 = paro_rot_destroy(r);
     return st != PARO_OK ? st : st2;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kNormMaxFeatures = 32768;
+
+// Checks shared by the two norms. An output may be exactly an fp16 input
+// (every element is read before it is written, by the same thread) and
+// nothing else: other overlaps would let one row's store change another
+// row's input.
+paro_status norm_impl(const void* X, int x_fp32, const void* R, const void* bias, const void* weight, float eps,
+                      void* H, void* Y, bool q8, int scale_group, float* S, int64_t T, int64_t F, paro_stream stream) {
+    g_err[0] = 0;
+    if (F <= 0 || F % 16) return fail(PARO_ERR_ARG, "features=%lld must be a positive multiple of 16", (long long)F);
+    if (F > kNormMaxFeatures)
+        return fail(PARO_ERR_UNSUPPORTED, "features=%lld > %lld", (long long)F, (long long)kNormMaxFeatures);
+    if (x_fp32 != 0 && x_fp32 != 1) return fail(PARO_ERR_ARG, "x_fp32=%d must be 0 or 1", x_fp32);
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(PARO_ERR_ARG, "eps must be positive and finite");
+    if (q8 && scale_group != 0 && scale_group != 128)
+        return fail(PARO_ERR_UNSUPPORTED, "scale_group=%d: 128 and 0 (one scale per row) are supported", scale_group);
+    if (T < 0) return fail(PARO_ERR_ARG, "tokens=%lld < 0", (long long)T);
+    if (T == 0) return PARO_OK;
+    if (T > (1LL << 40) / F || T > (1LL << 31) - 1) return fail(PARO_ERR_UNSUPPORTED, "tokens too large");
+    if (!X || !weight || !Y || (q8 && !S)) return fail(PARO_ERR_ARG, "null pointer");
+    if (!aligned16(X) || !aligned16(R) || !aligned16(bias) || !aligned16(weight) || !aligned16(H) || !aligned16(Y) ||
+        !aligned16(S))
+        return fail(PARO_ERR_ARG, "pointers must be 16-byte aligned");
+    const size_t n = (size_t)T * (size_t)F, nx = n * (x_fp32 ? 4 : 2);
+    const size_t ny = n * (q8 ? 1 : 2), ns = q8 ? (size_t)T * (scale_group ? (F + 127) / 128 : 1) * 4 : 0;
+    const struct { const void* p; size_t bytes; bool f16; } in[] = {
+        {X, nx, !x_fp32}, {R, n * 2, true}, {bias, (size_t)F * 2, false}, {weight, (size_t)F * 2, false}};
+    const struct { const void* p; size_t bytes; bool f16; const char* name; } o[] = {
+        {H, n * 2, true, "H"}, {Y, ny, !q8, "Y"}, {S, ns, false, "scales"}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& v : in)
+            if (overlap(o[i].p, o[i].bytes, v.p, v.bytes) && !(o[i].f16 && v.f16 && o[i].p == v.p))
+                return fail(PARO_ERR_ARG, "%s overlaps an input it may not share memory with", o[i].name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(o[i].p, o[i].bytes, o[j].p, o[j].bytes))
+                return fail(PARO_ERR_ARG, "%s and %s overlap", o[j].name, o[i].name);
+    }
+    cudaError_t e = paro::launch_rmsnorm(X, x_fp32 != 0, R, bias, weight, eps, H, Y, q8 ? S : nullptr, scale_group, T, F,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PARO_OK : cuda_fail(e, "rmsnorm launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+paro_status paro_rmsnorm(const void* X, int x_fp32, const void* R, const void* bias, const void* weight, float eps,
+                         void* H, void* Y, int64_t T, int64_t F, paro_stream stream) {
+    return norm_impl(X, x_fp32, R, bias, weight, eps, H, Y, false, 0, nullptr, T, F, stream);
+}
+
+paro_status paro_rmsnorm_q8(const void* X, int x_fp32, const void* R, const void* bias, const void* weight, float eps,
+                            int scale_group, void* H, void* Q, float* S, int64_t T, int64_t F, paro_stream stream) {
+    return norm_impl(X, x_fp32, R, bias, weight, eps, H, Q, true, scale_group, S, T, F, stream);
+}
+
+paro_status paro_q8_expand(const void* Q, const float* S, int scale_group, void* Y, int64_t T, int64_t F,
+                           paro_stream stream) {
+    g_err[0] = 0;
+    if (F <= 0 || F % 16) return fail(PARO_ERR_ARG, "features=%lld must be a positive multiple of 16", (long long)F);
+    if (F > kNormMaxFeatures)
+        return fail(PARO_ERR_UNSUPPORTED, "features=%lld > %lld", (long long)F, (long long)kNormMaxFeatures);
+    if (scale_group != 0 && scale_group != 128)
+        return fail(PARO_ERR_UNSUPPORTED, "scale_group=%d: 128 and 0 (one scale per row) are supported", scale_group);
+    if (T < 0) return fail(PARO_ERR_ARG, "tokens=%lld < 0", (long long)T);
+    if (T == 0) return PARO_OK;
+    if (T > ((1LL << 31) - 1) * 2048 / F) return fail(PARO_ERR_UNSUPPORTED, "tokens too large");   // one grid
+    if (!Q || !S || !Y) return fail(PARO_ERR_ARG, "null pointer");
+    if (!aligned16(Q) || !aligned16(S) || !aligned16(Y)) return fail(PARO_ERR_ARG, "pointers must be 16-byte aligned");
+    const size_t n = (size_t)T * (size_t)F;
+    if (overlap(Y, n * 2, Q, n) || overlap(Y, n * 2, S, (size_t)T * (scale_group ? (F + 127) / 128 : 1) * 4))
+        return fail(PARO_ERR_ARG, "Y overlaps an input");
+    cudaError_t e = paro::launch_q8_expand(Q, S, scale_group, Y, T, F, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PARO_OK : cuda_fail(e, "q8 expand launch");
 }
 
 }  // extern "C"

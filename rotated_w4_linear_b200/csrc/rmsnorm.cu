@@ -1,0 +1,346 @@
+// Root-mean-square norm between the layers, with the residual's addition:
+//
+//   v = x + b + r               (fp32; b and r optional)
+//   H = fp16(v)                 (the new residual stream)
+//   y = (v w) / sqrt(mean(v^2) + eps)
+//   Y = fp16(y), or the codes e4m3(y / s) with s = max|y| / 448 over 128
+//       channels or over the row
+//
+// x is fp16 (a layer's output) or fp32 (the summed shares of a row-parallel
+// layer: this kernel then also does the bias and the rounding that
+// paro_finalize does on its own). The norm is taken of the unrounded fp32 v,
+// so Y carries one rounding only.
+//
+// Bound: HBM, one pass. A row stays in registers from its loads to its
+// stores (VPT vectors of 8 channels per thread), so x and r are read once and
+// H and Y written once; the row's sum of squares and its largest |v w| (the
+// row's scale: max|y| = max|v w| / rms exactly, since one rounded product is
+// monotonic) share one cross-warp reduction in a fixed order, so a row's
+// result does not depend on the batch. A 128-channel group is sixteen
+// neighbouring lanes, so its scale is a four-step shuffle.
+// Measured (fp16 x, residual and H; HBM copy peak 6552 GB/s): 8192 x 4096
+// 45.0 us, 5970 GB/s; 4096 x 5120 with codes 29.3 us, 5000 GB/s; one token of
+// 4096 1.7 us, which is launch and latency. A persistent form with a
+// three-deep cp.async ring of rows ran slower (50.2 and 30.0 us): enough CTAs
+// are resident that one's loads cover another's reduction.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace paro {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+// smallest scale: keeps 1/s finite; an all-zero group has this scale and zero codes
+constexpr float kScaleFloor = 7.888609052210118e-31f;      // 2^-100
+
+struct NormArgs {
+    const void* x;               // fp16 or fp32 [T][F]
+    const __half* r;             // fp16 [T][F] or null
+    const __half* b;             // fp16 [F] or null
+    const __half* w;             // fp16 [F]
+    __half* H;                   // fp16 [T][F] or null (may be x or r)
+    void* Y;                     // fp16 or e4m3 [T][F]
+    float* S;                    // fp32 [T][nscale] (8-bit output)
+    int64_t T;
+    int nvec;                    // F / 8
+    int wpr;                     // warps per row
+    int rows;                    // rows per tile
+    float inv_f, eps;            // 1 / F
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float f[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float f[8]) {
+    return make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {   // a in the lowest byte
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+}  // namespace
+
+enum : int { kNormF16 = 0, kNormQ8Group = 1, kNormQ8Row = 2 };
+
+namespace {
+
+// A thread's place: warps wr of row rw of the CTA's tile of rows.
+struct NormPlace {
+    int lane, warp, rw, wr, t0, tr;
+};
+__device__ __forceinline__ NormPlace norm_place(const NormArgs& a) {
+    NormPlace p;
+    p.lane = threadIdx.x & 31;
+    p.warp = threadIdx.x >> 5;
+    p.rw = p.warp / a.wpr;
+    p.wr = p.warp - p.rw * a.wpr;
+    p.t0 = p.wr * 32 + p.lane;                             // first vector of the row, then every tr-th
+    p.tr = a.wpr * 32;
+    return p;
+}
+
+// The widest rows fetch the weights, which all rows share, when they need
+// them: 64 registers a thread do not hold them too.
+template <int VPT>
+struct NormWeights {
+    static constexpr bool kHold = VPT <= 2;
+    uint4 w[kHold ? VPT : 1];
+    __device__ __forceinline__ void load(const NormArgs& a, const NormPlace& p) {
+        if (kHold)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) w[j] = fetch(a, p.t0 + j * p.tr);
+    }
+    __device__ __forceinline__ uint4 get(const NormArgs& a, int j, int i) { return kHold ? w[j] : fetch(a, i); }
+    static __device__ __forceinline__ uint4 fetch(const NormArgs& a, int i) {
+        return i < a.nvec ? __ldg(reinterpret_cast<const uint4*>(a.w) + i) : make_uint4(0, 0, 0, 0);
+    }
+};
+
+// Everything after the loads, for one row: v[j] holds x of vector t0 + j tr
+// on entry (zeros outside the row), r its residual. Every thread of the CTA
+// calls it (it has a barrier).
+template <int VPT, int OUT>
+__device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, int64_t row, bool live,
+                                         float (&v)[VPT][8], const uint4 (&r)[VPT], NormWeights<VPT>& w,
+                                         float2* part) {
+    float ss = 0.f, mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = p.t0 + j * p.tr;
+        float f[8];
+        if (a.b && i < a.nvec) {
+            unpack8(__ldg(reinterpret_cast<const uint4*>(a.b) + i), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] += f[e];
+        }
+        unpack8(r[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] += f[e];
+        if (a.H && live && i < a.nvec) reinterpret_cast<uint4*>(a.H)[row * a.nvec + i] = pack8(v[j]);
+        unpack8(w.get(a, j, i), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss = fmaf(v[j][e], v[j][e], ss);
+            v[j][e] *= f[e];                               // v w from here on
+            if (OUT == kNormQ8Row) mx = fmaxf(mx, fabsf(v[j][e]));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (OUT == kNormQ8Row) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if (a.wpr > 1) {
+        if (p.lane == 0) part[p.warp] = make_float2(ss, mx);
+        __syncthreads();
+        const float2 q = p.lane < a.wpr ? part[p.rw * a.wpr + p.lane] : make_float2(0.f, 0.f);
+        ss = q.x;
+        mx = q.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (OUT == kNormQ8Row) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+    }
+    const float rms = 1.f / sqrtf(ss * a.inv_f + a.eps);
+    float inv_row = 0.f;
+    if (OUT == kNormQ8Row) {
+        const float s = fmaxf(mx * rms / kE4m3Max, kScaleFloor);
+        inv_row = 1.f / s;
+        if (live && p.wr == 0 && p.lane == 0) a.S[row] = s;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = p.t0 + j * p.tr;
+        const bool in = live && i < a.nvec;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = v[j][e] * rms;
+        if (OUT == kNormF16) {
+            if (in) static_cast<uint4*>(a.Y)[row * a.nvec + i] = pack8(y);
+        } else {
+            float inv = inv_row;
+            if (OUT == kNormQ8Group) {                     // lanes 0-15 and 16-31 are one group each
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+#pragma unroll
+                for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float s = fmaxf(m / kE4m3Max, kScaleFloor);
+                inv = 1.f / s;
+                if (in && (p.lane & 15) == 0) a.S[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s;
+            }
+            if (in)
+                static_cast<uint2*>(a.Y)[row * a.nvec + i] =
+                    make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+        }
+    }
+}
+
+template <bool X32>
+__device__ __forceinline__ void unpack_x(const uint4 (&x)[X32 ? 2 : 1], float v[8]) {
+    if (X32) {
+#pragma unroll
+        for (int h = 0; h < (X32 ? 2 : 1); ++h) {
+            v[4 * h] = __uint_as_float(x[h].x);
+            v[4 * h + 1] = __uint_as_float(x[h].y);
+            v[4 * h + 2] = __uint_as_float(x[h].z);
+            v[4 * h + 3] = __uint_as_float(x[h].w);
+        }
+    } else {
+        unpack8(x[0], v);
+    }
+}
+
+}  // namespace
+
+template <int VPT, bool X32, int OUT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+    // the next kernel may launch; it reads nothing of ours before this grid is complete
+    asm volatile("griddepcontrol.launch_dependents;");
+    constexpr int XV = X32 ? 2 : 1;
+    __shared__ float2 part[32];                            // per warp: sum of squares, largest |v w|
+    const NormPlace p = norm_place(a);
+    const int64_t row = (int64_t)blockIdx.x * a.rows + p.rw;
+    const bool live = row < a.T;
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // x and r may be the previous grid's output
+    // every load of the row in flight before any is used
+    uint4 x[VPT][XV], r[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = p.t0 + j * p.tr;
+        const bool in = live && i < a.nvec;
+        const int64_t at = row * a.nvec + i;
+#pragma unroll
+        for (int h = 0; h < XV; ++h) {
+            x[j][h] = make_uint4(0, 0, 0, 0);
+            if (in) x[j][h] = static_cast<const uint4*>(a.x)[at * XV + h];
+        }
+        r[j] = make_uint4(0, 0, 0, 0);
+        if (in && a.r) r[j] = reinterpret_cast<const uint4*>(a.r)[at];
+    }
+    NormWeights<VPT> w;
+    w.load(a, p);
+    float v[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) unpack_x<X32>(x[j], v[j]);
+    norm_row<VPT, OUT>(a, p, row, live, v, r, w, part);
+}
+
+// Codes and scales back to fp16: Y = fp16(code s). Eight channels per thread;
+// bound by HBM (3 bytes per channel).
+__global__ void q8_expand_kernel(const uint2* __restrict__ Q, const float* __restrict__ S, uint4* __restrict__ Y,
+                                 int nvec, int nscale, int64_t n) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (k >= n) return;
+    const int64_t row = k / nvec;
+    const int i = (int)(k - row * nvec);
+    const uint2 q = Q[k];
+    const float s = S[row * nscale + (nscale > 1 ? i >> 4 : 0)];
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {                          // two codes -> two fp16 (exact), then one rounded product
+        const uint16_t c = (uint16_t)((e < 2 ? q.x : q.y) >> (16 * (e & 1)));
+        uint32_t h2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+        y[2 * e] = f.x * s;
+        y[2 * e + 1] = f.y * s;
+    }
+    Y[k] = pack8(y);
+}
+
+namespace {
+
+cudaLaunchConfig_t pdl_config(unsigned grid, unsigned block, cudaStream_t s, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <int VPT, bool X32, int OUT>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg =
+        pdl_config((unsigned)((a.T + a.rows - 1) / a.rows), (unsigned)(32 * a.wpr * a.rows), s, &attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rmsnorm_kernel<VPT, X32, OUT>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int VPT>
+cudaError_t launch_norm_v(const NormArgs& a, bool x32, int out, cudaStream_t s) {
+    if (x32)
+        return out == kNormF16 ? launch_norm<VPT, true, kNormF16>(a, s)
+               : out == kNormQ8Group ? launch_norm<VPT, true, kNormQ8Group>(a, s)
+                                     : launch_norm<VPT, true, kNormQ8Row>(a, s);
+    return out == kNormF16 ? launch_norm<VPT, false, kNormF16>(a, s)
+           : out == kNormQ8Group ? launch_norm<VPT, false, kNormQ8Group>(a, s)
+                                 : launch_norm<VPT, false, kNormQ8Row>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const void* x, bool x_fp32, const void* r, const void* b, const void* w, float eps, void* H,
+                           void* Y, float* S, int scale_group, int64_t T, int64_t F, cudaStream_t s) {
+    if (T <= 0) return cudaSuccess;
+    NormArgs a{};
+    a.x = x;
+    a.r = static_cast<const __half*>(r);
+    a.b = static_cast<const __half*>(b);
+    a.w = static_cast<const __half*>(w);
+    a.H = static_cast<__half*>(H);
+    a.Y = Y;
+    a.S = S;
+    a.T = T;
+    a.nvec = (int)(F / 8);
+    a.inv_f = (float)(1.0 / (double)F);
+    a.eps = eps;
+    const int out = !S ? kNormF16 : scale_group ? kNormQ8Group : kNormQ8Row;
+    // The split of a row over threads goes by its width alone, so a row's
+    // sums have the same order in every batch. One vector per thread up to
+    // 4096 channels, then two (8192 x 4096: 45.0 us with one, 49.6 with two;
+    // 4096 x 5120 in 8 bits: 29.3 us with two, 35.3 with one), then four.
+    const int nw = (a.nvec + 31) / 32;                      // warps at one vector per thread
+    const int vpt = nw > 64 ? 4 : nw > 16 ? 2 : 1;
+    a.wpr = (nw + vpt - 1) / vpt;
+    a.rows = T > 296 && a.wpr < 8 ? 8 / a.wpr : 1;
+    return vpt == 4 ? launch_norm_v<4>(a, x_fp32, out, s)
+           : vpt == 2 ? launch_norm_v<2>(a, x_fp32, out, s)
+                      : launch_norm_v<1>(a, x_fp32, out, s);
+}
+
+cudaError_t launch_q8_expand(const void* Q, const float* S, int scale_group, void* Y, int64_t T, int64_t F,
+                             cudaStream_t s) {
+    if (T <= 0) return cudaSuccess;
+    const int nvec = (int)(F / 8);
+    const int64_t n = T * nvec;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)((n + 255) / 256), 256u, s, &attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, q8_expand_kernel, static_cast<const uint2*>(Q), S,
+                                             static_cast<uint4*>(Y), nvec,
+                                             scale_group ? (int)((F + 127) / 128) : 1, n);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace paro
