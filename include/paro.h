@@ -201,6 +201,66 @@ paro_status paro_linear_ex(const paro_rot* rot, const void* X_dev,
                            int64_t out_features, void* workspace_dev, size_t workspace_bytes,
                            paro_stream stream);
 
+/* Activations of the calls below: v; max(v, 0); v / (1 + e^-v); v Phi(v) (the
+ * error-function GELU); v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+typedef enum {
+    PARO_ACT_NONE = 0,
+    PARO_ACT_RELU = 1,
+    PARO_ACT_SILU = 2,
+    PARO_ACT_GELU = 3,
+    PARO_ACT_GELU_TANH = 4
+} paro_act;
+
+/* The layer with an activation and a residual in its epilogue:
+ *     Y = act((X T^-1) w_hat^T + b) + R
+ * with the bias, the activation and the residual applied to the fp32 sum
+ * before the single rounding to fp16. (The paper's layer is act none and R
+ * zero; a decoder block adds its attention output and down projections to
+ * the residual stream this way.)
+ *   bias_dev      fp16 [out_features] or NULL
+ *   residual_dev  R, fp16 [tokens][out_features] (16-byte aligned) or NULL; it
+ *                 may be Y_dev itself (Y += layer(X) in place)
+ *   act           a paro_act
+ * Y may share memory with the residual only, and only as the same pointer;
+ * the workspace shares none with X, the residual or Y (else PARO_ERR_ARG).
+ * Other arguments, workspace and errors as paro_linear_ex. Above 128 tokens
+ * the product runs on pairs of SMs (tcgen05 with cta_group::2). The result
+ * has the same bits in every call with the same arguments. */
+paro_status paro_linear_act(const paro_rot* rot, const void* X_dev,
+                            const void* qweight_dev, const void* scales_dev, const void* zeros_dev,
+                            const void* bias_dev, const void* residual_dev, int act, int group, void* Y_dev,
+                            int64_t tokens, int64_t in_features, int64_t out_features,
+                            void* workspace_dev, size_t workspace_bytes, paro_stream stream);
+
+/* Weights of a gated up-projection for paro_linear_gated: paro_pack_weights_ex
+ * with q uint8 [2 inter][in], s and z [2 inter][in/group], the gate's rows
+ * 0..inter-1 first and the up projection's after them (both quantised from
+ * the same T W). inter_features is a multiple of 8; the buffers have the sizes
+ * of paro_pack_size_ex for out_features = 2 inter. The format is the same
+ * except that every 16-row block holds eight gate rows and the eight up rows
+ * of the same channels, so it is not interchangeable with
+ * paro_pack_weights_ex's (paro_dequant_ex returns the rows in that order). */
+paro_status paro_pack_gated(const uint8_t* q, const uint16_t* s, const uint8_t* z,
+                            int64_t in_features, int64_t inter_features, int group,
+                            void* qweight_dev, void* scales_dev, void* zeros_dev, paro_stream stream);
+
+/* The gated up-projection of a feed-forward block in one product:
+ *     H = act((X T^-1) w_gate^T + b_gate) * ((X T^-1) w_up^T + b_up)
+ * from fp32 sums, rounded once to fp16; the 2 inter wide intermediate is
+ * never written.
+ *   qweight_dev, scales_dev, zeros_dev   from paro_pack_gated
+ *   bias_dev  fp16 [2 inter_features], the gate's first, or NULL
+ *   act       a paro_act
+ *   H_dev     fp16 [tokens][inter_features]; shares memory with no other buffer
+ * Workspace: paro_linear_workspace_size(tokens, in_features, 2
+ * inter_features). Other arguments and errors as paro_linear_ex, the bits of
+ * the result as paro_linear_act. */
+paro_status paro_linear_gated(const paro_rot* rot, const void* X_dev,
+                              const void* qweight_dev, const void* scales_dev, const void* zeros_dev,
+                              const void* bias_dev, int act, int group, void* H_dev,
+                              int64_t tokens, int64_t in_features, int64_t inter_features,
+                              void* workspace_dev, size_t workspace_bytes, paro_stream stream);
+
 /* Row-parallel use (several GPUs each holding a slice of the input channels,
  * cut on 128-channel boundaries): the group-diagonal T lets every rank
  * rotate only its own channels (paper notes, "independent rotation"), so a
@@ -311,7 +371,7 @@ paro_status paro_linear_once(const void* X_dev, const int16_t* pairs_host, const
 /* Fault word of the current device: 0, or the code of the first bounded wait
  * inside a tensor-core kernel that ran out (about 2 s) because a pipeline
  * stage never arrived: the kernel (0 prefill GEMM, 10 tensor-core rotation,
- * 20 its 256-channel form) plus the role (1 TMA producer, 2 MMA issuer,
+ * 20 its 256-channel form, 30 prefill GEMM on CTA pairs) plus the role (1 TMA producer, 2 MMA issuer,
  * 3 dequantisation, 4 epilogue, 5 a drain before exit); 6 is the self-test
  * below. The CTA that saw it raises an
  * abort flag in its shared memory: every role stops issuing copies and

@@ -20,6 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libparo.so")
 
 PARO_OK = 0
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # paro_act
 _STATUS = {0: "PARO_OK", 1: "PARO_ERR_ARG", 2: "PARO_ERR_UNSUPPORTED", 3: "PARO_ERR_CUDA", 4: "PARO_ERR_DEVICE"}
 
 _lib: Optional[ctypes.CDLL] = None
@@ -43,6 +44,9 @@ _SIGS = {
     "paro_linear_ex": [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "paro_linear_partial": [_vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "paro_finalize": [_vp, _vp, _vp, _i64, _i64, _vp],
+    "paro_linear_act": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
+    "paro_pack_gated": [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp],
+    "paro_linear_gated": [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
     "paro_rmsnorm": [_vp, _int, _vp, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _vp],
     "paro_rmsnorm_q8": [_vp, _int, _vp, _vp, _vp, _f32, _int, _vp, _vp, _vp, _i64, _i64, _vp],
     "paro_q8_expand": [_vp, _vp, _int, _vp, _i64, _i64, _vp],
@@ -334,40 +338,124 @@ def paro_linear_ex(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fea
     return Y
 
 
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _bias(bias: Optional[torch.Tensor], n: int) -> Optional[int]:
+    if bias is None:
+        return None
+    if bias.numel() != n:
+        raise ValueError(f"bias must have {n} elements")
+    return _dev(bias, torch.float16, "bias")
+
+
+def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int, act: str = "none",
+                    group: int = 128, bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                    Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = act((X T^-1) w_hat^T + bias) + residual, rounded once; Y may be the residual."""
+    a, b = _act(act), _bias(bias, out_features)
+    x = _dev(X, torch.float16, "X")
+    T, in_f = X.shape
+    shape = (T, out_features)
+    r = None if residual is None else _f16(residual, shape, X.get_device(), "residual")
+    Y = _out(Y, shape, torch.float16, X.device, "Y")
+    if ws is None:
+        ws = workspace(T, in_f, out_features, X.device)
+    with _on(X.device):
+        _check("paro_linear_act", lib().paro_linear_act(
+            rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
+            _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, r, a, group, Y.data_ptr(), T, in_f,
+            out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
+    return Y
+
+
+def paro_pack_gated(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=None, device=None, group: int = 128):
+    """Logical gate rows, then up rows (q uint8 [2 inter][in], s fp16 and z uint8
+    [2 inter][in/group]), on the device or on the host -> the device format of
+    paro_linear_gated (qweight, scales, zeros)."""
+    out_f, in_f = q.shape
+    if out_f % 2:
+        raise ValueError("q must hold as many up rows as gate rows")
+    if s.shape != (out_f, in_f // group) or z.shape != s.shape:
+        raise ValueError("s and z must be [2 inter][in/group]")
+    qb, sb, zb = paro_pack_size(in_f, out_f, group)
+    dev = device or (q.device if q.is_cuda else torch.device("cuda", torch.cuda.current_device()))
+    qw = torch.empty(qb, dtype=torch.uint8, device=dev)
+    sp = torch.empty(sb, dtype=torch.uint8, device=dev)
+    zp = torch.empty(zb, dtype=torch.uint8, device=dev)
+    with _on(qw.device):
+        _check("paro_pack_gated", lib().paro_pack_gated(
+            _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z"), in_f, out_f // 2, group,
+            qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
+    return qw, sp, zp
+
+
+def paro_linear_gated(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, inter_features: int, act: str = "silu",
+                      group: int = 128, bias: Optional[torch.Tensor] = None, H: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """H = act((X T^-1) w_gate^T + b_gate) * ((X T^-1) w_up^T + b_up), weights
+    from paro_pack_gated, bias [2 inter] (the gate's first)."""
+    a, b = _act(act), _bias(bias, 2 * inter_features)
+    x = _dev(X, torch.float16, "X")
+    T, in_f = X.shape
+    H = _out(H, (T, inter_features), torch.float16, X.device, "H")
+    if ws is None:
+        ws = workspace(T, in_f, 2 * inter_features, X.device)
+    with _on(X.device):
+        _check("paro_linear_gated", lib().paro_linear_gated(
+            rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
+            _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, a, group, H.data_ptr(), T, in_f,
+            inter_features, _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
+    return H
+
+
 class ParoLinear:
     """A prepared layer for repeated calls (a decode loop): the rotation
     handle, the packed weights, the bias and a workspace are checked once
-    here; a call checks only X and Y and hands raw pointers to the same C
-    entry point as paro_linear_ex. The workspace is owned by the object and
-    grows with the largest batch seen, so calls on one object must not
+    here; a call checks only X, Y and the residual and hands raw pointers to
+    the same C entry points as paro_linear_ex and paro_linear_act (the latter
+    with an activation or a residual). The workspace is owned by the object
+    and grows with the largest batch seen, so calls on one object must not
     overlap on the GPU (one stream, or events), as for paro_linear's
-    workspace. The object keeps references to the tensors it was given."""
+    workspace; a CUDA graph that captured a call keeps using the workspace of
+    that time, so the object must outlive the graph and see its largest batch
+    before the capture. The object keeps references to the tensors it was
+    given."""
+
+    _width_factor = 1                                   # rows of the weights per output column
 
     def __init__(self, rot: Optional[Rotation], qw, sp, zp, in_features: int, out_features: int, group: int = 128,
-                 bias: Optional[torch.Tensor] = None, device=None):
+                 bias: Optional[torch.Tensor] = None, device=None, act: str = "none"):
         if rot is not None and (rot.group != group or rot.in_features != in_features):
             raise ValueError("the rotation was prepared for another group size or input width")
         self.rot, self.in_features, self.out_features, self.group = rot, int(in_features), int(out_features), group
+        self.act = act
+        self._a = _act(act)
         self._tensors = (qw, sp, zp, bias)                 # kept alive for the pointers below
         self._h = rot.handle if rot is not None else None
         self._qw, self._sp, self._zp = _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), \
             _dev(zp, torch.uint8, "zeros")
-        self._b = None
-        if bias is not None:
-            if bias.numel() != out_features:
-                raise ValueError("bias must have out_features elements")
-            self._b = _dev(bias, torch.float16, "bias")
+        rows = self._width_factor * self.out_features
+        for t, need in zip((qw, sp, zp), paro_pack_size(self.in_features, rows, group)):
+            if t.numel() < need:
+                raise ValueError(f"packed weights of {t.numel()} bytes, {need} needed for this shape and group")
+        self._b = _bias(bias, rows)
         self.device = qw.device if device is None else torch.device(device)
         self._ws = None
         self._ws_tokens = 0
         self._f = lib().paro_linear_ex
+        self._f_act = lib().paro_linear_act
 
     def _workspace(self, T: int) -> None:
-        if T > self._ws_tokens:
-            self._ws = workspace(T, self.in_features, self.out_features, self.device)
+        if T > self._ws_tokens or self._ws is None:
+            self._ws = workspace(T, self.in_features, self._width_factor * self.out_features, self.device)
             self._ws_tokens = T
 
-    def __call__(self, X: torch.Tensor, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    def _prepare(self, X, Y, stream):
+        """(tokens, Y, raw stream) of a call, after its checks."""
         T = X.shape[0]
         if not X.is_cuda or X.dtype is not torch.float16 or not X.is_contiguous() or X.dim() != 2 \
                 or X.shape[1] != self.in_features:
@@ -376,17 +464,48 @@ class ParoLinear:
             Y = torch.empty((T, self.out_features), dtype=torch.float16, device=X.device)
         elif not Y.is_cuda or Y.dtype is not torch.float16 or not Y.is_contiguous() or Y.numel() != T * self.out_features:
             raise TypeError(f"Y must be a contiguous fp16 CUDA tensor [tokens][{self.out_features}]")
-        if T > self._ws_tokens:
+        if T > self._ws_tokens or self._ws is None:
             self._workspace(T)
         if stream is None:
-            sp = int(_raw_stream(X.get_device())) if _raw_stream is not None else _stream(None, X.device)
-        else:
-            sp = _stream(stream, X.device)
-        st = self._f(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, self.group, Y.data_ptr(), T,
-                     self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
+            return T, Y, int(_raw_stream(X.get_device())) if _raw_stream is not None else _stream(None, X.device)
+        return T, Y, _stream(stream, X.device)
+
+    def __call__(self, X: torch.Tensor, Y: Optional[torch.Tensor] = None, stream=None,
+                 residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        T, Y, sp = self._prepare(X, Y, stream)
+        if residual is None and self._a == 0:
+            st = self._f(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, self.group, Y.data_ptr(), T,
+                         self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
+            if st != PARO_OK:
+                _check("paro_linear_ex", st)
+            return Y
+        r = None if residual is None else _f16(residual, (T, self.out_features), X.get_device(), "residual")
+        st = self._f_act(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, r, self._a, self.group,
+                         Y.data_ptr(), T, self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
         if st != PARO_OK:
-            _check("paro_linear_ex", st)
+            _check("paro_linear_act", st)
         return Y
+
+
+class ParoGated(ParoLinear):
+    """The prepared form of paro_linear_gated: weights from paro_pack_gated,
+    bias [2 inter_features]; a call returns H [tokens][inter_features]."""
+
+    _width_factor = 2
+
+    def __init__(self, rot: Optional[Rotation], qw, sp, zp, in_features: int, inter_features: int, group: int = 128,
+                 bias: Optional[torch.Tensor] = None, device=None, act: str = "silu"):
+        super().__init__(rot, qw, sp, zp, in_features, inter_features, group, bias, device, act)
+        self.inter_features = self.out_features
+        self._f_gated = lib().paro_linear_gated
+
+    def __call__(self, X: torch.Tensor, H: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        T, H, sp = self._prepare(X, H, stream)
+        st = self._f_gated(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, self._a, self.group,
+                           H.data_ptr(), T, self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
+        if st != PARO_OK:
+            _check("paro_linear_gated", st)
+        return H
 
 
 def paro_linear_partial(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int, group: int = 128,

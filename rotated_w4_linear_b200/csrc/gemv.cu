@@ -26,8 +26,9 @@
 //     fp16 multiply: w_hat = fp16((q - z) s)) straight into an m16n8k16 A
 //     fragment; the B fragment (four consecutive channels of one token) comes
 //     from shared memory; fp32 accumulation in two independent chains, added
-//     into the CTA's partial tile [token][row] (shared-memory atomics) when
-//     the warp's run leaves a row block;
+//     into the CTA's partial tile [token][row] when the warp's run leaves a
+//     row block; where warps share a row block their sums are added in warp
+//     order (no atomics: the same bits in every call);
 //   split-k: after a cluster barrier CTA x sums its slice of the rows over
 //     the cluster's tiles with distributed shared memory loads and stores it
 //     as fp16. No global atomics, no workspace.
@@ -41,6 +42,7 @@
 #include <tuple>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 
 namespace paro {
@@ -52,6 +54,7 @@ constexpr int kStages = 3;
 constexpr int kMaxSplit = 16;                             // largest cluster (k-chunks per row tile)
 constexpr int kItemGroups = 2;                            // 128-channel groups per item
 constexpr int kItemQBytes = kItemGroups * 2 * 512;        // int4 codes
+constexpr int kJoinStride = 20;                           // floats per token of a joining warp's sums
 // GS: quantisation groups per 128 channels (1: group 128, 2: group 64); an
 // item carries codes, then GS scale words x 8 per group, then GS zero bytes x 8
 template <int GS>
@@ -71,6 +74,8 @@ struct GemvArgs {
     const __half* bias;   // [out] fp16 or null
     __half* Y;            // fp16 [T][out], or
     float* Yf;            // fp32 [T][out] unrounded sums (row-parallel partials) when not null
+    const __half* residual;   // kEpiAct: fp16 [T][out] or null (may be Y)
+    int act;              // kEpiAct, kEpiGated: the activation
     int xlm;              // X' already lane-major within 64-channel blocks
 };
 
@@ -162,7 +167,7 @@ __device__ __forceinline__ void issue_item(const ItemSrc& p, uint32_t slot, uint
 
 }  // namespace
 
-template <int NT, int GS>
+template <int NT, int GS, int EPI>
 __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) {
     constexpr int kItemBytes = item_bytes<GS>();
     // When the next kernel on the stream may launch (it prefetches only its
@@ -271,7 +276,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
             }
         }
         cp_async_commit();
-        for (int i = threadIdx.x; i < NT * 8 * SR; i += kWarps * 32) red[i] = 0.f;
         cp_async_wait<0>();                                // (the first weight items are in by now too)
     }
     __syncthreads();
@@ -292,15 +296,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
+    // A row block's units may be shared by several warps. The warp that has
+    // its first unit stores its sums into the CTA's tile; a warp whose run
+    // begins inside a row block keeps that block's sums in registers until its
+    // run is over (its ring is free then) and leaves them there, to be added
+    // in warp order: no atomics, the same bits in every call.
+    const bool joins = ncg > 0 && f_hi > f_lo && f_lo != rbl_lo * ncg;
+    float first[NT][4];
     auto flush = [&](int rbl) {
         float* base = red + rbl * 16 + gq;
+        const bool keep = joins && rbl == rbl_lo;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = nt * 8 + 2 * qd + e;
-                atomicAdd(base + t * SR, acc[nt][0][e] + acc[nt][1][e]);
-                atomicAdd(base + t * SR + 8, acc[nt][0][2 + e] + acc[nt][1][2 + e]);
+            for (int e = 0; e < 4; ++e) {                  // token 2 qd + (e & 1), row gq + 8 (e >> 1)
+                const float v = acc[nt][0][e] + acc[nt][1][e];
+                if (keep) first[nt][e] = v;
+                else base[(nt * 8 + 2 * qd + (e & 1)) * SR + 8 * (e >> 1)] = v;
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
@@ -376,20 +388,96 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     if (pending) flush(c_rbl);                             // run ended inside a row block
     if (NT == 2) asm volatile("griddepcontrol.launch_dependents;");
     cp_async_wait<0>();
+    if (joins) {                                           // [token][16 rows], 20 floats apart (conflict-free)
+        __syncwarp();
+        float* own = reinterpret_cast<float*>(ring + (size_t)warp * kStages * kItemBytes);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                own[(nt * 8 + 2 * qd + (e & 1)) * kJoinStride + gq + 8 * (e >> 1)] = first[nt][e];
+    }
     __syncthreads();
+
+    // The tile's sum for token t, rows r..r+3 of the tile (r a multiple of 4):
+    // the stored sums plus those of the warps that joined the row block.
+    const int nrows_tile = nrbt * 16;
+    const int row0 = rb_begin * 16;
+    auto tile_sum4 = [&](int t, int r) {
+        float4 v = *reinterpret_cast<const float4*>(red + t * SR + r);
+        const int rb = r >> 4, f0 = rb * ncg;
+        for (int w = max(1, kWarps * rb / max(nrbt, 1)); w < kWarps; ++w) {
+            const int lo = (int)(((int64_t)F * w) / kWarps);
+            if (lo >= f0 + ncg) break;
+            if (lo <= f0 || lo == (int)(((int64_t)F * (w + 1)) / kWarps)) continue;   // owns the block, or has no run
+            const float4 u = *reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(ring + (size_t)w * kStages * kItemBytes) + t * kJoinStride + (r & 15));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        return v;
+    };
+    // ---- epilogue of four finished sums (rows r..r+3 of the tile, token t),
+    // or of four gate sums v and their four up sums u
+    auto bias4 = [&](int c) {
+        return a.bias ? make_float4(__half2float(a.bias[c]), __half2float(a.bias[c + 1]), __half2float(a.bias[c + 2]),
+                                    __half2float(a.bias[c + 3]))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto finish = [&](int t, int r, float4 v, float4 u) {
+        if (EPI == kEpiGated) {
+            // tile rows 16 b + e (gate) and 16 b + 8 + e (up), e < 8, are column 8 b + e of H
+            const int c = ((row0 + r) >> 4) * 8 + (r & 7), width = a.out >> 1;
+            const float4 bg = bias4(c), bu = bias4(a.bias ? width + c : c);
+            const float h0 = act_any(v.x + bg.x, a.act) * (u.x + bu.x), h1 = act_any(v.y + bg.y, a.act) * (u.y + bu.y);
+            const float h2 = act_any(v.z + bg.z, a.act) * (u.z + bu.z), h3 = act_any(v.w + bg.w, a.act) * (u.w + bu.w);
+            *reinterpret_cast<uint2*>(a.Y + (size_t)t * width + c) = make_uint2(pack_half2(h0, h1), pack_half2(h2, h3));
+            return;
+        }
+        const float4 b = bias4(row0 + r);
+        v.x += b.x;
+        v.y += b.y;
+        v.z += b.z;
+        v.w += b.w;
+        const size_t at = (size_t)t * a.out + row0 + r;
+        if (EPI == kEpiAct) {
+            v = make_float4(act_any(v.x, a.act), act_any(v.y, a.act), act_any(v.z, a.act), act_any(v.w, a.act));
+            if (a.residual) {
+                const uint2 w = *reinterpret_cast<const uint2*>(a.residual + at);
+                const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+                v.x += lo.x;
+                v.y += lo.y;
+                v.z += hi.x;
+                v.w += hi.y;
+            }
+        }
+        if (EPI == kEpiPlain && a.Yf)
+            *reinterpret_cast<float4*>(a.Yf + at) = v;
+        else
+            *reinterpret_cast<uint2*>(a.Y + at) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+    };
+    // A thread's k-th four rows of `n4` fours: for the gated epilogue the k-th
+    // four gate rows (two fours in each 16-row block)
+    constexpr int kFours = EPI == kEpiGated ? 2 : 4;       // fours per row block that a thread may take
+    auto four = [&](int k) { return EPI == kEpiGated ? (k >> 1) * 16 + (k & 1) * 4 : 4 * k; };
 
     // ---- split-k: CTA x of the cluster sums its share of the rows over all
     // the cluster's tiles (distributed shared memory loads) and stores fp16
-    const int nrows_tile = nrbt * 16;
-    const int row0 = rb_begin * 16;
     if (a.nsplit == 1) {
-        for (int i = threadIdx.x; i < a.T * nrows_tile; i += kWarps * 32) {
-            const int t = i / nrows_tile, r = i - t * nrows_tile;
-            const float b = a.bias ? __half2float(a.bias[row0 + r]) : 0.f;
-            if (a.Yf) a.Yf[(size_t)t * a.out + row0 + r] = red[t * SR + r] + b;
-            else a.Y[(size_t)t * a.out + row0 + r] = __float2half_rn(red[t * SR + r] + b);
+        const int n4 = nrbt * kFours;
+        for (int i = threadIdx.x; i < a.T * n4; i += kWarps * 32) {
+            const int t = i / n4, r = four(i - t * n4);
+            finish(t, r, tile_sum4(t, r), EPI == kEpiGated ? tile_sum4(t, r + 8) : make_float4(0.f, 0.f, 0.f, 0.f));
         }
         return;
+    }
+    // the joining warps' sums go into the tile before the other CTAs read it
+    for (int i = threadIdx.x; i < a.T * nrbt * 4; i += kWarps * 32) {
+        const int t = i / (nrbt * 4), r = 4 * (i - t * nrbt * 4);
+        *reinterpret_cast<float4*>(red + t * SR + r) = tile_sum4(t, r);
     }
     cluster_sync();
     const int rlo = chunk * a.share;
@@ -397,9 +485,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     const uint32_t red_local = smem_u32(red);
     // four rows per thread (n is a multiple of 16); the loads from all the
     // cluster's tiles are issued before any is used, so their latencies overlap
-    const int n4 = n >> 2;
-    for (int i = threadIdx.x; i < a.T * n4; i += kWarps * 32) {
-        const int t = i / n4, r = rlo + 4 * (i - t * n4);
+    auto cluster_sum4 = [&](int t, int r) {
         const uint32_t off = red_local + (uint32_t)(t * SR + r) * 4u;
         float4 part[kMaxSplit];
 #pragma unroll
@@ -414,17 +500,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
                 sum.z += part[x].z;
                 sum.w += part[x].w;
             }
-        if (a.bias) {
-            sum.x += __half2float(a.bias[row0 + r]);
-            sum.y += __half2float(a.bias[row0 + r + 1]);
-            sum.z += __half2float(a.bias[row0 + r + 2]);
-            sum.w += __half2float(a.bias[row0 + r + 3]);
-        }
-        if (a.Yf)
-            *reinterpret_cast<float4*>(a.Yf + (size_t)t * a.out + row0 + r) = sum;
-        else
-            *reinterpret_cast<uint2*>(a.Y + (size_t)t * a.out + row0 + r) =
-                make_uint2(pack_half2(sum.x, sum.y), pack_half2(sum.z, sum.w));
+        return sum;
+    };
+    const int n4 = (n >> 4) * kFours;
+    for (int i = threadIdx.x; i < a.T * n4; i += kWarps * 32) {
+        const int t = i / n4, r = rlo + four(i - t * n4);
+        finish(t, r, cluster_sum4(t, r), EPI == kEpiGated ? cluster_sum4(t, r + 8) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
     cluster_sync_relaxed();                                // tiles stay alive until every reader is done
 }
@@ -444,7 +525,7 @@ size_t gemv_smem(int NT, int GS, int KC, int RT) {
 // CTAs of one launch that can be resident at once: clusters of `nsplit` CTAs
 // must sit inside one GPC, so for nsplit > 1 this is the driver's count of
 // co-resident clusters times nsplit (fewer than SMs x CTAs per SM).
-template <int NT, int GS>
+template <int NT, int GS, int EPI>
 int gemv_slots(int dev, int nsplit, int per_sm) {
     static std::mutex mu;
     static std::map<std::tuple<int, int, int>, int> cache;
@@ -455,7 +536,7 @@ int gemv_slots(int dev, int nsplit, int per_sm) {
     int sms = 148;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     int slots = sms * per_sm;
-    if (nsplit > 1 && cudaFuncSetAttribute(gemv_kernel<NT, GS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+    if (nsplit > 1 && cudaFuncSetAttribute(gemv_kernel<NT, GS, EPI>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                           cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(nsplit, 1024, 1);
@@ -469,9 +550,9 @@ int gemv_slots(int dev, int nsplit, int per_sm) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int nc = 0;
-        if (cudaFuncSetAttribute(gemv_kernel<NT, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
+        if (cudaFuncSetAttribute(gemv_kernel<NT, GS, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
                 cudaSuccess &&
-            cudaOccupancyMaxActiveClusters(&nc, gemv_kernel<NT, GS>, &cfg) == cudaSuccess && nc > 0)
+            cudaOccupancyMaxActiveClusters(&nc, gemv_kernel<NT, GS, EPI>, &cfg) == cudaSuccess && nc > 0)
             slots = std::min(slots, nc * nsplit);
         cudaGetLastError();   // a refused query leaves the SM-count estimate
     }
@@ -481,7 +562,7 @@ int gemv_slots(int dev, int nsplit, int per_sm) {
 
 // Choose (k-chunk, row tile) for one shape: minimise waves x (items per warp
 // + pipeline fill), counting only CTAs that can be resident together.
-template <int NT, int GS>
+template <int NT, int GS, int EPI>
 GemvPlan plan_gemv(int dev, int64_t in, int64_t out, int T, int K) {
     const int G = (int)(in / 128);
     const int nrb = (int)(out / 16);
@@ -504,7 +585,7 @@ GemvPlan plan_gemv(int dev, int64_t in, int64_t out, int T, int K) {
             // runs before this one
             if (smem + kReserved + rot_reserve > kSmemPerSm) break;
             const int per_sm = 1;
-            const int slots = gemv_slots<NT, GS>(dev, ns, per_sm);
+            const int slots = gemv_slots<NT, GS, EPI>(dev, ns, per_sm);
             const int rowtiles = (nrb + RT - 1) / RT;
             const int ctas = ns * rowtiles;
             const int waves = (ctas + slots - 1) / slots;
@@ -532,18 +613,18 @@ GemvPlan plan_gemv(int dev, int64_t in, int64_t out, int T, int K) {
     return best;
 }
 
-template <int NT, int GS>
+template <int NT, int GS, int EPI>
 GemvPlan cached_plan(int dev, int64_t in, int64_t out, int T, int K) {
     static std::mutex mu;
     static std::map<std::tuple<int, int64_t, int64_t, int, int>, GemvPlan> cache;
     std::lock_guard<std::mutex> lock(mu);
     const auto key = std::make_tuple(dev, in, out, T, K);
     auto it = cache.find(key);
-    if (it == cache.end()) it = cache.emplace(key, plan_gemv<NT, GS>(dev, in, out, T, K)).first;
+    if (it == cache.end()) it = cache.emplace(key, plan_gemv<NT, GS, EPI>(dev, in, out, T, K)).first;
     return it->second;
 }
 
-template <int NT, int GS>
+template <int NT, int GS, int EPI>
 cudaError_t launch_gemv_t(const GemvArgs& a, const GemvPlan& p, int dev, cudaStream_t s) {
     // kernel attributes, set once per device (double-checked under a lock)
     static std::atomic<bool> configured[64] = {};
@@ -553,9 +634,9 @@ cudaError_t launch_gemv_t(const GemvArgs& a, const GemvPlan& p, int dev, cudaStr
         std::lock_guard<std::mutex> lock(mu);
         if (!configured[dev].load(std::memory_order_relaxed)) {
             cudaError_t e =
-                cudaFuncSetAttribute(gemv_kernel<NT, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+                cudaFuncSetAttribute(gemv_kernel<NT, GS, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(gemv_kernel<NT, GS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                e = cudaFuncSetAttribute(gemv_kernel<NT, GS, EPI>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             configured[dev].store(true, std::memory_order_release);
         }
@@ -576,7 +657,25 @@ cudaError_t launch_gemv_t(const GemvArgs& a, const GemvPlan& p, int dev, cudaStr
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, GS>, a);
+    return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, GS, EPI>, a);
+}
+
+// Plan and launch for one token-tile count, group size and epilogue.
+template <int NT, int GS, int EPI>
+cudaError_t launch_gemv_epi(GemvArgs& a, int dev, int K, cudaStream_t s) {
+    const GemvPlan p = cached_plan<NT, GS, EPI>(dev, a.in, a.out, a.T, K);
+    a.KC = p.KC;
+    a.RT = p.RT;
+    a.nsplit = p.nsplit;
+    a.share = p.share;
+    return launch_gemv_t<NT, GS, EPI>(a, p, dev, s);
+}
+
+template <int NT, int GS>
+cudaError_t launch_gemv_any(GemvArgs& a, int epi, int dev, int K, cudaStream_t s) {
+    return epi == kEpiGated ? launch_gemv_epi<NT, GS, kEpiGated>(a, dev, K, s)
+           : epi == kEpiAct ? launch_gemv_epi<NT, GS, kEpiAct>(a, dev, K, s)
+                            : launch_gemv_epi<NT, GS, kEpiPlain>(a, dev, K, s);
 }
 
 }  // namespace
@@ -586,7 +685,7 @@ cudaError_t launch_gemv_t(const GemvArgs& a, const GemvPlan& p, int dev, cudaStr
 // launches, so the decode kernel's weight stream starts during the rotation.
 cudaError_t launch_gemv(const RotDev* rot, const void* X, const void* qw, const void* scp, const void* zp,
                         const void* bias, void* Y, int64_t T, int64_t in, int64_t out, int group, void* ws,
-                        cudaStream_t s, bool y_fp32) {
+                        cudaStream_t s, bool y_fp32, const Epilogue& epi) {
     if (T <= 0) return cudaSuccess;
     if (group != 64 && group != 128) return cudaErrorInvalidValue;
     const bool g64 = group == 64;
@@ -605,8 +704,6 @@ cudaError_t launch_gemv(const RotDev* rot, const void* X, const void* qw, const 
         xr = ws;
         lane_major = true;
     }
-    const GemvPlan p = (T > 8) ? (g64 ? cached_plan<2, 2>(dev, in, out, (int)T, K) : cached_plan<2, 1>(dev, in, out, (int)T, K))
-                               : (g64 ? cached_plan<1, 2>(dev, in, out, (int)T, K) : cached_plan<1, 1>(dev, in, out, (int)T, K));
     GemvArgs a{};
     a.Xr = static_cast<const __half*>(xr);
     a.T = (int)T;
@@ -615,19 +712,17 @@ cudaError_t launch_gemv(const RotDev* rot, const void* X, const void* qw, const 
     a.G = (int)(in / 128);
     a.Gq = (int)(in / group);
     a.Gqp = a.Gq + (a.Gq & 1);
-    a.KC = p.KC;
-    a.RT = p.RT;
-    a.nsplit = p.nsplit;
-    a.share = p.share;
     a.qw = static_cast<const uint4*>(qw);
     a.sp = static_cast<const uint32_t*>(scp);
     a.zp = static_cast<const uint8_t*>(zp);
     a.bias = static_cast<const __half*>(bias);
     a.Y = y_fp32 ? nullptr : static_cast<__half*>(Y);
     a.Yf = y_fp32 ? static_cast<float*>(Y) : nullptr;
+    a.residual = static_cast<const __half*>(epi.residual);
+    a.act = epi.act;
     a.xlm = lane_major ? 1 : 0;
-    cudaError_t e = (T > 8) ? (g64 ? launch_gemv_t<2, 2>(a, p, dev, s) : launch_gemv_t<2, 1>(a, p, dev, s))
-                            : (g64 ? launch_gemv_t<1, 2>(a, p, dev, s) : launch_gemv_t<1, 1>(a, p, dev, s));
+    const cudaError_t e = T > 8 ? (g64 ? launch_gemv_any<2, 2>(a, epi.kind, dev, K, s) : launch_gemv_any<2, 1>(a, epi.kind, dev, K, s))
+                                : (g64 ? launch_gemv_any<1, 2>(a, epi.kind, dev, K, s) : launch_gemv_any<1, 1>(a, epi.kind, dev, K, s));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -7,6 +7,15 @@
 
 namespace paro {
 
+// What a layer's kernel does with its sums (epilogue.cuh): kind kEpiPlain,
+// kEpiAct (act, residual) or kEpiGated (act; `out` counts gate and up rows,
+// Y has out / 2 columns).
+struct Epilogue {
+    int kind = 0;
+    int act = 0;
+    const void* residual = nullptr;   // fp16 [T][out] or null; may be Y
+};
+
 struct RotDev {
     int64_t in = 0;         // input features
     int G = 0;              // groups of 128 (tables are built per 128 channels)
@@ -46,7 +55,7 @@ size_t rotate_decode_smem(int K, int T);
 
 // group: channels per quantisation group (128 or 64) of the weight format.
 cudaError_t launch_pack(const uint8_t* q, const uint16_t* sc, const uint8_t* z, int64_t in, int64_t out, int group,
-                        void* qw, void* scp, void* zp, cudaStream_t s);
+                        void* qw, void* scp, void* zp, cudaStream_t s, bool gated = false);
 cudaError_t launch_dequant(const void* qw, const void* scp, const void* zp, int64_t in, int64_t out, int group,
                            void* W, cudaStream_t s);
 cudaError_t launch_quantize(const RotDev& r, const void* W, int64_t out, uint8_t* q, uint16_t* sc,
@@ -58,7 +67,7 @@ cudaError_t launch_quantize(const RotDev& r, const void* W, int64_t out, uint8_t
 // y_fp32: Y is fp32 and receives the unrounded sums (row-parallel partials).
 cudaError_t launch_gemv(const RotDev* rot, const void* X, const void* qw, const void* scp, const void* zp,
                         const void* bias, void* Y, int64_t T, int64_t in, int64_t out, int group, void* ws,
-                        cudaStream_t s, bool y_fp32 = false);
+                        cudaStream_t s, bool y_fp32 = false, const Epilogue& epi = Epilogue());
 
 // Decode with the X' scratch in a static device array (no allocation anywhere).
 size_t noalloc_scratch_bytes();
@@ -69,7 +78,11 @@ cudaError_t launch_gemv_noalloc(const RotDev* rot, const void* X, const void* qw
 // launched as a programmatic dependent of the rotation kernel.
 // group: channels per quantisation group of the weights (128 or 64).
 cudaError_t launch_gemm(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
-                        int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, bool y_fp32 = false);
+                        int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, bool y_fp32 = false,
+                        const Epilogue& epi = Epilogue());
+// Prefill above 128 tokens on CTA pairs (gemm_pair_sm100.cu): the same product with 256-row x 256-token tiles.
+cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
+                             int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, const Epilogue& epi);
 
 // Y16 = fp16(Yf + bias) (bias fp16 [out] or null): the last step of a
 // row-parallel layer after the partial sums were added across ranks.
@@ -87,7 +100,10 @@ cudaError_t launch_q8_expand(const void* Q, const float* S, int scale_group, voi
 // A kernel whose bounded wait runs out on purpose after limit_ns (fault code 6).
 cudaError_t launch_wait_selftest(uint64_t limit_ns, cudaStream_t s);
 
-// Fault code left by a bounded wait that ran out (0 = none); optionally cleared.
-cudaError_t read_fault(unsigned int* code, bool clear);
+// Fault code left by a bounded wait that ran out (0 = none); optionally
+// cleared. Every source file with bounded waits has a fault word of its own.
+cudaError_t read_fault_gemm(unsigned int* code, bool clear);
+cudaError_t read_fault_gemm_pair(unsigned int* code, bool clear);
+cudaError_t read_fault_rotate(unsigned int* code, bool clear);
 
 }  // namespace paro

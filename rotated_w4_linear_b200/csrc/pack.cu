@@ -8,7 +8,15 @@ namespace paro {
 // ---------------------------------------------------------------------------
 // pack: one thread per 32-bit word of the device format (layout in common.cuh)
 // ---------------------------------------------------------------------------
-__global__ void pack_q_kernel(const uint8_t* __restrict__ q, uint32_t* __restrict__ qw, int in, int64_t nwords) {
+// Source rows of rows g and g + 8 of row block rb. inter = 0: rows in order.
+// Gated layers (inter output channels): the logical tensors hold the gate's
+// rows 0..inter-1, then the up projection's; a row block holds eight of each,
+// so that a channel's gate and up sums meet in one tile.
+__device__ __forceinline__ int64_t pack_row0(int64_t rb, int g, int inter) { return (inter ? rb * 8 : rb * 16) + g; }
+__device__ __forceinline__ int64_t pack_row1(int64_t row0, int inter) { return row0 + (inter ? inter : 8); }
+
+__global__ void pack_q_kernel(const uint8_t* __restrict__ q, uint32_t* __restrict__ qw, int in, int inter,
+                              int64_t nwords) {
     const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (w >= nwords) return;
     const int nkb = in / 64;
@@ -19,8 +27,9 @@ __global__ void pack_q_kernel(const uint8_t* __restrict__ q, uint32_t* __restric
     const int64_t rb = blk / nkb;
     const int g = lane >> 2, qd = lane & 3;
     const int k0 = kb * 64 + j * 16 + 4 * qd;
-    const uint8_t* r0 = q + (rb * 16 + g) * (int64_t)in + k0;
-    const uint8_t* r1 = r0 + 8 * (int64_t)in;
+    const int64_t row0 = pack_row0(rb, g, inter);
+    const uint8_t* r0 = q + row0 * in + k0;
+    const uint8_t* r1 = q + pack_row1(row0, inter) * in + k0;
     // nibble slot -> (row, k offset): 0:(r0,0) 4:(r0,1) 1:(r0,2) 5:(r0,3) 2:(r1,0) 6:(r1,1) 3:(r1,2) 7:(r1,3)
     uint32_t word = 0;
     word |= (uint32_t)(r0[0] & 0xF) << 0;
@@ -38,7 +47,8 @@ __global__ void pack_q_kernel(const uint8_t* __restrict__ q, uint32_t* __restric
 // logical s, z have Gsrc = G / rep groups per row (rep = 2 for groups of 256,
 // whose scale and zero are repeated for both 128-channel halves)
 __global__ void pack_meta_kernel(const uint16_t* __restrict__ s, const uint8_t* __restrict__ z,
-                                 uint32_t* __restrict__ sp, uint8_t* __restrict__ zp, int G, int rep, int64_t n) {
+                                 uint32_t* __restrict__ sp, uint8_t* __restrict__ zp, int G, int rep, int inter,
+                                 int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;   // (rb, gi, g)
     if (i >= n) return;
     const int Gp = G + (G & 1), Gsrc = G / rep;
@@ -46,7 +56,7 @@ __global__ void pack_meta_kernel(const uint16_t* __restrict__ s, const uint8_t* 
     const int64_t rg = i >> 3;
     const int gi = (int)(rg % G);
     const int64_t rb = rg / G;
-    const int64_t r0 = rb * 16 + g, r1 = r0 + 8;
+    const int64_t r0 = pack_row0(rb, g, inter), r1 = pack_row1(r0, inter);
     const int gs = gi / rep;
     sp[i] = (uint32_t)s[r0 * Gsrc + gs] | ((uint32_t)s[r1 * Gsrc + gs] << 16);
     const uint8_t zb = (uint8_t)((z[r0 * Gsrc + gs] & 0xF) | ((z[r1 * Gsrc + gs] & 0xF) << 4));
@@ -55,16 +65,17 @@ __global__ void pack_meta_kernel(const uint16_t* __restrict__ s, const uint8_t* 
 }
 
 cudaError_t launch_pack(const uint8_t* q, const uint16_t* sc, const uint8_t* z, int64_t in, int64_t out, int group,
-                        void* qw, void* scp, void* zp, cudaStream_t s) {
+                        void* qw, void* scp, void* zp, cudaStream_t s, bool gated) {
+    const int inter = gated ? (int)(out / 2) : 0;
     const int64_t nwords = in * out / 8;
     if (nwords > 0)
-        pack_q_kernel<<<(unsigned)((nwords + 255) / 256), 256, 0, s>>>(q, static_cast<uint32_t*>(qw), (int)in, nwords);
+        pack_q_kernel<<<(unsigned)((nwords + 255) / 256), 256, 0, s>>>(q, static_cast<uint32_t*>(qw), (int)in, inter, nwords);
     const int rep = group == 256 ? 2 : 1;                      // group 256: stored as group 128
     const int G = (int)(in / (group == 256 ? 128 : group));
     const int64_t nm = (out / 16) * G * 8;
     if (nm > 0)
         pack_meta_kernel<<<(unsigned)((nm + 255) / 256), 256, 0, s>>>(sc, z, static_cast<uint32_t*>(scp),
-                                                                      static_cast<uint8_t*>(zp), G, rep, nm);
+                                                                      static_cast<uint8_t*>(zp), G, rep, inter, nm);
     return cudaGetLastError();
 }
 

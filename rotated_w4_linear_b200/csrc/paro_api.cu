@@ -12,6 +12,7 @@
 
 #include "../../include/paro.h"
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 
 struct paro_rot {
@@ -175,10 +176,16 @@ paro_status paro_linear_noalloc(const paro_rot* r, const void* X, const void* qw
 paro_status paro_fault_status(int* code, int clear) {
     g_err[0] = 0;
     if (!code) return fail(PARO_ERR_ARG, "code is null");
-    unsigned int c = 0;
-    cudaError_t e = paro::read_fault(&c, clear != 0);
-    if (e != cudaSuccess) return cuda_fail(e, "read fault word");
-    *code = (int)c;
+    // one word per source file with bounded waits; the first that is set is reported
+    cudaError_t (*const words[])(unsigned int*, bool) = {paro::read_fault_gemm, paro::read_fault_gemm_pair,
+                                                         paro::read_fault_rotate};
+    *code = 0;
+    for (auto* read : words) {
+        unsigned int c = 0;
+        const cudaError_t e = read(&c, clear != 0);
+        if (e != cudaSuccess) return cuda_fail(e, "read fault word");
+        if (*code == 0) *code = (int)c;
+    }
     return PARO_OK;
 }
 
@@ -509,8 +516,12 @@ paro_status paro_pack_size(int64_t in, int64_t out, size_t* qb, size_t* sb, size
     return paro_pack_size_ex(in, out, 128, qb, sb, zb);
 }
 
-paro_status paro_pack_weights_ex(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t in, int64_t out,
-                                 int group, void* qw, void* sp, void* zp, paro_stream stream) {
+}  // extern "C"
+
+namespace {
+
+paro_status pack_impl(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t in, int64_t out, int group,
+                      void* qw, void* sp, void* zp, paro_stream stream, bool gated) {
     g_err[0] = 0;
     paro_status st = check_shape(in, out);
     if (st != PARO_OK) return st;
@@ -521,7 +532,7 @@ paro_status paro_pack_weights_ex(const uint8_t* q, const uint16_t* s, const uint
     if (!aligned16(qw) || !aligned16(sp) || !aligned16(zp)) return fail(PARO_ERR_ARG, "outputs must be 16-byte aligned");
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (!is_unregistered_host(q) && !is_unregistered_host(s) && !is_unregistered_host(z)) {
-        cudaError_t e = paro::launch_pack(q, s, z, in, out, group, qw, sp, zp, cs);
+        cudaError_t e = paro::launch_pack(q, s, z, in, out, group, qw, sp, zp, cs, gated);
         return e == cudaSuccess ? PARO_OK : cuda_fail(e, "pack launch");
     }
     // host inputs: stage the logical tensors in one temporary device buffer
@@ -537,11 +548,34 @@ paro_status paro_pack_weights_ex(const uint8_t* q, const uint16_t* s, const uint
     if (e == cudaSuccess) e = cudaMemcpyAsync(tmp + oz, z, nz, cudaMemcpyDefault, cs);
     if (e == cudaSuccess)
         e = paro::launch_pack(reinterpret_cast<const uint8_t*>(tmp + oq), reinterpret_cast<const uint16_t*>(tmp + os_),
-                              reinterpret_cast<const uint8_t*>(tmp + oz), in, out, group, qw, sp, zp, cs);
+                              reinterpret_cast<const uint8_t*>(tmp + oz), in, out, group, qw, sp, zp, cs, gated);
     const cudaError_t e2 = cudaStreamSynchronize(cs);
     cudaFree(tmp);
     if (e != cudaSuccess) return cuda_fail(e, "pack from host memory");
     return e2 == cudaSuccess ? PARO_OK : cuda_fail(e2, "pack from host memory (synchronize)");
+}
+
+// inter: a multiple of 8, so that gate and up rows fill whole 16-row blocks
+paro_status check_inter(int64_t inter) {
+    if (inter <= 0 || inter % 8) return fail(PARO_ERR_ARG, "inter_features=%lld must be a positive multiple of 8", (long long)inter);
+    if (inter > (1LL << 21)) return fail(PARO_ERR_UNSUPPORTED, "shape too large");
+    return PARO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+paro_status paro_pack_weights_ex(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t in, int64_t out,
+                                 int group, void* qw, void* sp, void* zp, paro_stream stream) {
+    return pack_impl(q, s, z, in, out, group, qw, sp, zp, stream, false);
+}
+
+paro_status paro_pack_gated(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t in, int64_t inter, int group,
+                            void* qw, void* sp, void* zp, paro_stream stream) {
+    g_err[0] = 0;
+    paro_status st = check_inter(inter);
+    return st != PARO_OK ? st : pack_impl(q, s, z, in, 2 * inter, group, qw, sp, zp, stream, true);
 }
 
 paro_status paro_pack_weights(const uint8_t* q, const uint16_t* s, const uint8_t* z, int64_t in, int64_t out,
@@ -596,7 +630,8 @@ namespace {
 // The layer: fp16 Y, or (y_fp32) the unrounded fp32 sums of a row-parallel slice.
 paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const void* sp, const void* zp,
                         const void* bias, int group, void* Y, int64_t T, int64_t in, int64_t out, void* ws,
-                        size_t ws_bytes, paro_stream stream, bool y_fp32) {
+                        size_t ws_bytes, paro_stream stream, bool y_fp32,
+                        const paro::Epilogue& epi = paro::Epilogue()) {
     g_err[0] = 0;
     paro_status st = check_shape(in, out);
     if (st != PARO_OK) return st;
@@ -618,11 +653,23 @@ paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const 
     size_t need = 0;
     paro_linear_workspace_size(T, in, out, &need);
     if (ws_bytes < need) return fail(PARO_ERR_ARG, "workspace_bytes=%zu < %zu", ws_bytes, need);
+    if (epi.kind != paro::kEpiPlain) {
+        // the output may be exactly the residual and shares no memory with anything else that is read or written
+        const size_t nx = (size_t)T * in * 2, ny = (size_t)T * (epi.kind == paro::kEpiGated ? out / 2 : out) * 2;
+        const void* R = epi.residual;
+        if (!aligned16(R)) return fail(PARO_ERR_ARG, "pointers must be 16-byte aligned");
+        if (overlap(Y, ny, X, nx) || overlap(Y, ny, ws, need) || overlap(Y, ny, bias, (size_t)out * 2) ||
+            overlap(Y, ny, qw, (size_t)in * out / 2))
+            return fail(PARO_ERR_ARG, "the output overlaps an input or the workspace");
+        if (R != Y && overlap(R, ny, Y, ny)) return fail(PARO_ERR_ARG, "residual and output overlap without being the same");
+        if (overlap(ws, need, X, nx) || overlap(ws, need, R, ny) || overlap(ws, need, bias, (size_t)out * 2))
+            return fail(PARO_ERR_ARG, "the workspace overlaps an input");
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const paro::RotDev* rd = r ? &r->dev : nullptr;
     cudaError_t e;
     if (T <= 16) {   // decode rotation kernel into ws, then the int4 decode kernel
-        e = paro::launch_gemv(rd, X, qw, sp, zp, bias, Y, T, in, out, fmt_group, ws, s, y_fp32);
+        e = paro::launch_gemv(rd, X, qw, sp, zp, bias, Y, T, in, out, fmt_group, ws, s, y_fp32, epi);
         return e == cudaSuccess ? PARO_OK : cuda_fail(e, "decode launch");
     }
     // X' = X T^-1 into the workspace, then the tensor-core GEMM as a
@@ -633,7 +680,7 @@ paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const 
         if (e != cudaSuccess) return cuda_fail(e, "rotate launch");
         src = ws;
     }
-    e = paro::launch_gemm(src, qw, sp, zp, bias, Y, T, in, out, fmt_group, s, y_fp32);
+    e = paro::launch_gemm(src, qw, sp, zp, bias, Y, T, in, out, fmt_group, s, y_fp32, epi);
     return e == cudaSuccess ? PARO_OK : cuda_fail(e, "prefill launch");
 }
 
@@ -645,6 +692,31 @@ paro_status paro_linear_ex(const paro_rot* r, const void* X, const void* qw, con
                            const void* bias, int group, void* Y, int64_t T, int64_t in, int64_t out, void* ws,
                            size_t ws_bytes, paro_stream stream) {
     return linear_impl(r, X, qw, sp, zp, bias, group, Y, T, in, out, ws, ws_bytes, stream, false);
+}
+
+paro_status paro_linear_act(const paro_rot* r, const void* X, const void* qw, const void* sp, const void* zp,
+                            const void* bias, const void* residual, int act, int group, void* Y, int64_t T, int64_t in,
+                            int64_t out, void* ws, size_t ws_bytes, paro_stream stream) {
+    g_err[0] = 0;
+    if (act < 0 || act >= paro::kActCount) return fail(PARO_ERR_ARG, "act=%d is not a paro_act", act);
+    paro::Epilogue epi;
+    epi.kind = paro::kEpiAct;
+    epi.act = act;
+    epi.residual = residual;
+    return linear_impl(r, X, qw, sp, zp, bias, group, Y, T, in, out, ws, ws_bytes, stream, false, epi);
+}
+
+paro_status paro_linear_gated(const paro_rot* r, const void* X, const void* qw, const void* sp, const void* zp,
+                              const void* bias, int act, int group, void* H, int64_t T, int64_t in, int64_t inter,
+                              void* ws, size_t ws_bytes, paro_stream stream) {
+    g_err[0] = 0;
+    if (act < 0 || act >= paro::kActCount) return fail(PARO_ERR_ARG, "act=%d is not a paro_act", act);
+    paro_status st = check_inter(inter);
+    if (st != PARO_OK) return st;
+    paro::Epilogue epi;
+    epi.kind = paro::kEpiGated;
+    epi.act = act;
+    return linear_impl(r, X, qw, sp, zp, bias, group, H, T, in, 2 * inter, ws, ws_bytes, stream, false, epi);
 }
 
 paro_status paro_linear_partial(const paro_rot* r, const void* X, const void* qw, const void* sp, const void* zp,

@@ -526,4 +526,6 @@ cudaError_t launch_rotate_tc(const RotDev& r, const void* X, void* Xr, int64_t T
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+cudaError_t read_fault_rotate(unsigned int* code, bool clear) { return read_fault_word(code, clear); }
+
 }  // namespace paro

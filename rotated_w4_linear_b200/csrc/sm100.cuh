@@ -10,16 +10,23 @@
 
 namespace paro {
 
-// 0 = no fault; otherwise a code naming the wait that timed out (one per
-// translation unit that includes this header; the library has one).
+// 0 = no fault; otherwise a code naming the wait that timed out (one word per
+// translation unit that includes this header, read by read_fault_word there).
 static __device__ unsigned int g_paro_fault = 0;
 
+static inline cudaError_t read_fault_word(unsigned int* code, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_paro_fault, sizeof(unsigned int));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_paro_fault, &zero, sizeof(unsigned int));
+}
+
 // (kernel offset + role): prefill GEMM 0, tensor-core rotation 10, its
-// 256-channel form 20; roles 1 TMA producer, 2 MMA issuer, 3 dequantisation,
+// 256-channel form 20, CTA-pair GEMM 30; roles 1 TMA producer, 2 MMA issuer, 3 dequantisation,
 // 4 epilogue, 5 a drain before exit; 6 the self-test
 enum : unsigned int { kFaultTmaWait = 1, kFaultMmaWait = 2, kFaultDequantWait = 3, kFaultEpilogueWait = 4,
                       kFaultDrainWait = 5, kFaultSelfTest = 6 };
-enum : unsigned int { kFaultGemm = 0, kFaultRotate = 10, kFaultRotate256 = 20 };
+enum : unsigned int { kFaultGemm = 0, kFaultRotate = 10, kFaultRotate256 = 20, kFaultGemmPair = 30 };
 
 // Time limit of a pipeline wait: far above any stage of a correct kernel.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -74,3 +74,56 @@ def test_expand_refusals(L):
     refused(L, call(S=None), ARG, "null")
     refused(L, call(Q=P[0] + 4), ARG, "aligned")
     assert call(T=0, Q=None) == 0
+
+
+def act(L, rot=None, X=P[0], qw=P[1], s=P[2], z=P[3], b=P[4], R=P[5], act=2, group=128, Y=P[6], T=4, n_in=256, n_out=64,
+        ws=P[7], wsb=1 << 20):
+    return L.paro_linear_act(rot, X, qw, s, z, b, R, act, group, Y, T, n_in, n_out, ws, wsb, None)
+
+
+def gated(L, rot=None, X=P[0], qw=P[1], s=P[2], z=P[3], b=P[4], act=2, group=128, H=P[6], T=4, n_in=256, inter=32,
+          ws=P[7], wsb=1 << 20):
+    return L.paro_linear_gated(rot, X, qw, s, z, b, act, group, H, T, n_in, inter, ws, wsb, None)
+
+
+@pytest.mark.parametrize("call", [act, gated])
+def test_layer_refusals(L, call):
+    for a in (-1, 5, 99):
+        refused(L, call(L, act=a), ARG, "act")
+    refused(L, call(L, n_in=200), ARG, "in_features")
+    refused(L, call(L, group=32), UNSUPPORTED, "group")
+    refused(L, call(L, group=256, n_in=384), ARG, "multiple of 256")
+    refused(L, call(L, T=-1), ARG, "tokens")
+    refused(L, call(L, T=1 << 30), UNSUPPORTED, "tokens")
+    refused(L, call(L, wsb=16), ARG, "workspace_bytes")
+    for name in ("X", "qw", "s", "z", "ws"):
+        refused(L, call(L, **{name: None}), ARG, "null")
+        refused(L, call(L, **{name: P[8] + 8}), ARG, "aligned")
+    refused(L, call(L, b=P[4] + 1), ARG, "bias")
+    assert call(L, T=0, X=None) == 0
+
+
+def test_layer_overlaps(L):
+    n = 4 * 64 * 2
+    refused(L, act(L, R=P[5] + 4), ARG, "aligned")
+    refused(L, act(L, Y=P[0] + 16), ARG, "overlaps an input")
+    refused(L, act(L, Y=P[7]), ARG, "workspace")
+    refused(L, act(L, Y=P[4]), ARG, "overlaps an input")
+    refused(L, act(L, Y=P[1] + 32), ARG, "overlaps an input")
+    refused(L, act(L, R=P[6] + n - 16), ARG, "residual")
+    refused(L, act(L, R=P[6] - 16), ARG, "residual")
+    refused(L, act(L, ws=P[0]), ARG, "workspace")
+    refused(L, act(L, ws=P[5]), ARG, "workspace")
+    refused(L, gated(L, H=P[0]), ARG, "overlaps an input")
+    refused(L, gated(L, H=P[7] + 64), ARG, "workspace")
+
+
+def test_gated_widths(L):
+    for inter in (0, -8, 4, 12, 33):
+        refused(L, gated(L, inter=inter), ARG, "inter_features")
+        refused(L, L.paro_pack_gated(P[0], P[1], P[2], 256, inter, 128, P[3], P[4], P[5], None), ARG, "inter_features")
+    refused(L, gated(L, inter=1 << 22), UNSUPPORTED, "large")
+    refused(L, L.paro_pack_gated(None, P[1], P[2], 256, 32, 128, P[3], P[4], P[5], None), ARG, "null")
+    refused(L, L.paro_pack_gated(P[0], P[1], P[2], 250, 32, 128, P[3], P[4], P[5], None), ARG, "in_features")
+    refused(L, L.paro_pack_gated(P[0], P[1], P[2], 256, 32, 32, P[3], P[4], P[5], None), UNSUPPORTED, "group")
+    refused(L, L.paro_pack_gated(P[0], P[1], P[2], 256, 32, 128, P[3] + 8, P[4], P[5], None), ARG, "aligned")
