@@ -17,9 +17,10 @@
 //              (they arrive while the last MMAs run); at the end it stores
 //              the finished tile with TMA, 64 tokens at a time;
 //   warp 1     tensor memory; in the leader CTA one lane issues the MMAs
-//              (A from tensor memory, B from shared memory) once both CTAs'
-//              sixteen dequantisation warps have reported the stage, and
-//              commits each stage back to both CTAs' producers;
+//              (A from tensor memory, B from shared memory) once its eight
+//              dequantisation warps and the other CTA have reported the
+//              stage, and commits it back to both CTAs' producers; in the
+//              other CTA one lane forwards its eight warps' reports;
 //   warps 2-9  dequantise (w_hat = fp16((q - z) s), as the other kernels do):
 //              a warp takes one quarter of the rows and one half of the
 //              stage's channels; then the epilogue: the same quarter of the
@@ -206,7 +207,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(afull0 + 8 * s, 16);                // the dequantisation warps of both CTAs (leader's is used)
+            mbar_init(afull0 + 8 * s, rank == 0 ? 9 : 8); // this CTA's dequantisation warps (leader: and the other CTA)
             mbar_init(free0 + 8 * s, 1);
         }
         mbar_init(done, 1);
@@ -297,12 +298,20 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 umma_commit_pair(free0 + 8 * s);
             }
             umma_commit_pair(done);                       // always: arrives once every MMA issued above has completed
+        } else if (lane == 0) {
+            // the other CTA reports a stage once, for its eight warps: a
+            // cluster-scope release by each of them cost 900 cycles a stage
+            const uint32_t leader_afull0 = map_to_rank(afull0, 0);
+            for (int i = 0; i < nk; ++i) {
+                const int s = i % S, u = i / S;
+                if (!mbar_wait(afull0 + 8 * s, u & 1, kFaultGemmPair + kFaultMmaWait, abort)) break;
+                mbar_arrive_cluster(leader_afull0 + 8 * s);
+            }
         }
     } else {
         const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
         const int half = (warp - 2) >> 2;                 // channels 64 half .. of a stage, then tokens 128 half ..
         const int g = lane >> 2;
-        const uint32_t leader_afull0 = map_to_rank(afull0, 0);
         for (int i = 0; i < nk; ++i) {
             const int s = i % S, u = i / S;
             // the tensor-memory stores below are warp-collective: the whole
@@ -326,7 +335,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_afull0 + 8 * s);
+            if (lane == 0) mbar_arrive(afull0 + 8 * s);
         }
 
         // ---- epilogue: one accumulator row per thread, tokens 128 half .. + 127
