@@ -2,39 +2,44 @@
 // with an activation and a residual and for the gated up-projection:
 //   Y^T tile [256 rows][256 tokens] = w_hat * X'^T, then the epilogue.
 //
-// The single-CTA kernel (gemm_sm100.cu) loads a 256-token X' tile for 128
-// rows: 36 KB per 64 channels and SM, and its time is that traffic's, not the
-// tensor pipe's. Here two CTAs of a cluster share the tile: each keeps its
-// own 128 rows of w_hat in its tensor memory and holds half of the tokens in
-// shared memory, and one MMA (M = 256, N = 256, K = 16) reads both halves, so
-// an SM loads 20 KB per 64 channels for the same work.
-//
-// Per CTA, ten warps, a ring of four stages of 128 channels:
-//   warp 0     TMA producer: per stage the CTA's 128 tokens of X' (two
-//              64-channel boxes, 128-byte swizzle), the int4 codes of its 8
-//              row blocks, their scales and zeros; then the residual's two
-//              128-row x 128-token tiles into the next two stages of the ring
-//              (they arrive while the last MMAs run); at the end it stores
-//              the finished tile with TMA, 64 tokens at a time;
-//   warp 1     tensor memory; in the leader CTA one lane issues the MMAs
-//              (A from tensor memory, B from shared memory) once its eight
-//              dequantisation warps and the other CTA have reported the
-//              stage, and commits it back to both CTAs' producers; in the
-//              other CTA one lane forwards its eight warps' reports;
-//   warps 2-9  dequantise (w_hat = fp16((q - z) s), as the other kernels do):
-//              a warp takes one quarter of the rows and one half of the
-//              stage's channels; then the epilogue: the same quarter of the
-//              rows and one half of the tokens, from tensor memory through
-//              registers into shared memory as fp16 [token][row].
-// Tensor memory: 256 columns of fp32 sums, 4 x 64 columns of w_hat (all 512).
+// Two CTAs of a cluster share a tile: each keeps its own 128 rows of w_hat in
+// its tensor memory and holds half of the tokens in shared memory, and one
+// MMA (M = 256, N = 256, K = 16) reads both halves. The kernel is persistent:
+// a cluster walks the tiles cid, cid + clusters, ... (row tiles first, so that
+// the clusters at work share their tokens), and its roles run ahead of each
+// other across tiles. Per CTA, nineteen warps:
+//   warp 0      TMA producer of X': per stage of 128 channels the CTA's 128
+//               tokens (two 64-channel boxes, 128-byte swizzle), ring of 4;
+//   warp 2      TMA producer of the weights: the stage's int4 codes of 8 row
+//               blocks with their scales and zeros, ring of 6: they are small,
+//               so they run further ahead than X', and the dequantisation of
+//               a stage does not wait behind its X' load;
+//   warps 3-10  dequantise (w_hat = fp16((q - z) s), as the other kernels do)
+//               into a ring of 4 tensor-memory stages: a warp takes one
+//               quarter of the rows and one half of the stage's channels;
+//   warp 1      tensor memory; in the leader CTA one lane issues the MMAs
+//               (A from tensor memory, B from shared memory) once its
+//               dequantisation warps and the other CTA have reported the
+//               stage, and commits it back to both CTAs; in the other CTA one
+//               lane forwards its CTA's reports;
+//   warps 11-18 epilogue: a warp takes one quarter of the rows and one half of
+//               the tokens, 64 tokens at a time from tensor memory into
+//               registers (after the second 64 the accumulator is free for
+//               the next tile), then through a 32-token buffer of its own in
+//               shared memory, where the residual has arrived by TMA, to a TMA
+//               store.
+// Tensor memory: 256 columns of fp32 sums, 4 x 64 columns of w_hat (all 512),
+// so there is one accumulator: the MMAs pause from a tile's last commit until
+// its sums are in registers.
 // All waits are bounded (sm100.cuh); a wait that runs out raises the CTA's
-// abort flag, what was issued is drained, both CTAs meet at the last cluster
-// barrier and nothing is stored.
+// abort flag, every role stops, what was issued is drained, and both CTAs meet
+// at the last cluster barrier.
 //
 // A token's result does not depend on its place in the batch: the order of
 // the channels goes by the row tile alone.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -47,18 +52,20 @@ namespace paro {
 
 namespace {
 
-constexpr int kPairStages = 4;
-constexpr int kPairThreads = 320;
+constexpr int kXStages = 4, kWStages = 6;
+constexpr int kPairThreads = 608;
 constexpr uint32_t kHalfX = 128 * 128;                  // 128 tokens x 64 channels
-constexpr uint32_t kPairX = 2 * kHalfX;                 // 32 KB: 128 tokens x 128 channels
-constexpr uint32_t kPairW = 8 * 1024;                   // 8 row blocks x 128 channels of codes
-constexpr uint32_t kPairS = 8 * 64;                     // scales: 8 row blocks x up to 2 groups x 8 words
-constexpr uint32_t kPairZ = 8 * 16;                     // zeros: 8 row blocks x 2 groups x 8 bytes
-constexpr uint32_t kPairStage = kPairX + kPairW + kPairS + kPairZ;
-constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + 256;
+constexpr uint32_t kXStage = 2 * kHalfX;                // 32 KB: 128 tokens x 128 channels
+constexpr uint32_t kWCodes = 8 * 1024;                  // 8 row blocks x 128 channels of codes
+constexpr uint32_t kWScales = 8 * 64;                   // 8 row blocks x up to 2 groups x 8 words
+constexpr uint32_t kWStage = kWCodes + kWScales + 128;  // zeros: 8 row blocks x 2 groups x 8 bytes
+constexpr uint32_t kOutBuf = 32 * 64;                   // 32 tokens x 32 rows of fp16: two for each epilogue warp
+constexpr uint32_t kPairBars = 8 * (4 * kXStages + 2 * kWStages + 8 + 16) + 16;
+constexpr size_t kPairSmem = 1024 + (size_t)kXStages * kXStage + (size_t)kWStages * kWStage + 16 * kOutBuf + kPairBars;
 
 struct PairArgs {
     int T, out, nk;             // nk: 128-channel stages
+    int mt, ntiles;             // 256-row tiles; tiles in all
     int width;                  // columns of Y (out, or out / 2 for the gated epilogue)
     int gs;                     // quantisation groups per 128 channels (1, or 2 for group 64)
     int act, has_res;
@@ -78,25 +85,29 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrive at a barrier of the cluster's other CTA, and wait for such arrivals.
+// Relaxed: what they order is tensor memory (written with tcgen05.st, read by
+// the MMA), which goes by the tcgen05 fences on both sides, and shared memory
+// that TMA wrote and the MMA reads; no ordinary loads and stores meet here. A
+// release at cluster scope costs about 900 cycles.
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait_other(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// mbar_wait for a barrier at which the other CTA's threads arrive too
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned int fault,
-                                                  volatile uint32_t* abort) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_other(uint32_t bar, uint32_t parity, unsigned int fault,
+                                                volatile uint32_t* abort) {
+    if (mbar_try_wait_other(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait_other(bar, parity)) return true;
         if ((it & 255u) == 0) {
             if (*abort) return false;
             if (global_ns() - t0 > kWaitLimitNs) {
@@ -139,29 +150,29 @@ __device__ __forceinline__ float lds16(uint32_t addr) {
 }
 
 // 32 tokens of one accumulator row per thread: the sums become fp16 in the
-// tile [token][128 rows], over the residual where there is one.
+// warp's buffer [token][32 rows], over the residual where there is one.
 struct PairAct {
     const uint32_t* r;
     float b;
-    uint32_t at;                // this row in the first token's row of the tile (256 bytes per token)
+    uint32_t at;                // this row in the buffer's first token (64 bytes per token)
     bool has_res;
     template <int ACT>
     __device__ __forceinline__ void run() const {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             float v = act_fn<ACT>(__uint_as_float(r[j]) + b);
-            if (has_res) v += lds16(at + j * 256);
-            sts16(at + j * 256, v);
+            if (has_res) v += lds16(at + j * 64);
+            sts16(at + j * 64, v);
         }
     }
 };
 // Gate rows (lanes with bit 3 clear) and up rows (8 lanes on) trade columns:
-// of tokens t, t + 1 the gate lane finishes t, the up lane t + 1. Tile
-// [token][64 channels], 128 bytes per token.
+// of tokens t, t + 1 the gate lane finishes t, the up lane t + 1. Buffer
+// [token][16 channels], 32 bytes per token.
 struct PairGated {
     const uint32_t* r;
     float b;                    // this row's own bias
-    uint32_t at;                // this lane's channel in the first token's row of the tile
+    uint32_t at;                // this lane's channel in the buffer's first token (up lanes: second token)
     bool up;
     template <int ACT>
     __device__ __forceinline__ void run() const {
@@ -169,7 +180,20 @@ struct PairGated {
         for (int j = 0; j < 32; j += 2) {
             const float v0 = __uint_as_float(r[j]) + b, v1 = __uint_as_float(r[j + 1]) + b;
             const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-            sts16(at + (j + (up ? 1 : 0)) * 128, act_fn<ACT>(up ? other : v0) * (up ? v1 : other));
+            sts16(at + j * 32, act_fn<ACT>(up ? other : v0) * (up ? v1 : other));
+        }
+    }
+};
+
+// A ring position: slot and use count of the i-th item, advanced one by one.
+template <int N>
+struct RingPos {
+    int slot = 0;
+    uint32_t use = 0;           // uses of this slot before the current one
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            ++use;
         }
     }
 };
@@ -182,37 +206,41 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_z,
                  const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
                  const PairArgs a) {
-    constexpr int S = kPairStages;
+    // the next kernel's CTAs may take SMs as this grid's leave them; it reads
+    // nothing of ours before this grid is complete
+    asm volatile("griddepcontrol.launch_dependents;");
     constexpr uint32_t kIdesc = umma_idesc_f16(256, 256);
-    constexpr uint32_t kTokenBytes = EPI == kEpiGated ? 128 : 256;     // one token of the finished tile
+    constexpr uint32_t kTokenBytes = EPI == kEpiGated ? 32 : 64;       // one token of an epilogue warp's buffer
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t sX = smem_addr(smem), sW = sX + S * kPairX, sS = sW + S * kPairW, sZ = sS + S * kPairS;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)S * kPairStage);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 3 * S + 7);
+    const uint32_t sX = smem_addr(smem), sOut = sX + kXStages * kXStage, sW = sOut + 16 * kOutBuf;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)kXStages * kXStage + 16 * kOutBuf + (size_t)kWStages * kWStage);
+    const uint32_t xfull0 = smem_addr(bars), free0 = xfull0 + 8 * kXStages, afull0 = free0 + 8 * kXStages;
+    const uint32_t afwd0 = afull0 + 8 * kXStages, wfull0 = afwd0 + 8 * kXStages, wfree0 = wfull0 + 8 * kWStages;
+    const uint32_t accfull = wfree0 + 8 * kWStages, accfree = accfull + 8, fin = accfree + 8, rfull0 = fin + 8;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 4 * kXStages + 2 * kWStages + 8 + 16);
     volatile uint32_t* abort = tslot + 1;
-    const uint32_t full0 = smem_addr(bars), afull0 = full0 + 8 * S, free0 = afull0 + 8 * S;
-    const uint32_t done = free0 + 8 * S, rfull0 = done + 8, ready0 = rfull0 + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int rb0 = blockIdx.x * 8, n0 = blockIdx.y * 256;
-    const int nk = a.nk;
-    // Pairs walk the channels from different starting stages, so that
-    // concurrent requests spread over the memory channels; the start goes by
-    // the row tile alone.
-    const int kstart = (int)((((blockIdx.x >> 1) * 0x9E3779B1u) >> 16) % (uint32_t)nk);
-    auto kstage = [&](int i) { const int j = i + kstart; return j >= nk ? j - nk : j; };
+    const int nclusters = gridDim.x >> 1, nk = a.nk;
+    const int first_tile = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, 1);
-            mbar_init(afull0 + 8 * s, rank == 0 ? 9 : 8); // this CTA's dequantisation warps (leader: and the other CTA)
-            mbar_init(free0 + 8 * s, 1);
+        for (int s = 0; s < kXStages; ++s) {
+            mbar_init(xfull0 + 8 * s, 1);
+            mbar_init(free0 + 8 * s, 1);                  // the MMAs on X' stage and w_hat stage s are done
+            mbar_init(afull0 + 8 * s, 8);                 // this CTA's dequantisation warps
+            mbar_init(afwd0 + 8 * s, 1);                  // leader: the other CTA's report
         }
-        mbar_init(done, 1);
-        for (int h = 0; h < 2; ++h) mbar_init(rfull0 + 8 * h, 1);
-        for (int c = 0; c < 4; ++c) mbar_init(ready0 + 8 * c, 4);
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(wfull0 + 8 * s, 1);
+            mbar_init(wfree0 + 8 * s, 8);
+        }
+        mbar_init(accfull, 1);
+        mbar_init(accfree, 8);                            // this CTA's epilogue warps have the sums
+        mbar_init(fin, 1);
+        for (int r = 0; r < 16; ++r) mbar_init(rfull0 + 8 * r, 1);
         *abort = 0u;
         mbar_fence_init();
         tma_prefetch_desc(&tm_x);
@@ -220,6 +248,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         tma_prefetch_desc(&tm_s);
         tma_prefetch_desc(&tm_z);
         tma_prefetch_desc(&tm_y);
+        if (EPI == kEpiAct) tma_prefetch_desc(&tm_r);
     }
     if (warp == 1) tmem_alloc_pair(smem_addr(tslot), 512);
     tc_fence_before();
@@ -231,148 +260,229 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     // X' is written by the rotation grid launched just before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // The ring's slots after the last stage hold the residual and then the
-    // finished tile: half h (tokens 128 h .. + 127) is in slot (nk + h) mod S.
-    auto tile_slot = [&](int h) { return sX + (uint32_t)((nk + h) % S) * kPairX; };
+    // tile -> row blocks of this CTA, first token, first channel stage.
+    // Clusters walk the channels from different starting stages, so that
+    // concurrent requests spread over the memory channels; the start goes by
+    // the row tile alone.
+    auto row_block0 = [&](int tile) { return ((tile % a.mt) * 2 + (int)rank) * 8; };
+    auto token0 = [&](int tile) { return tile / a.mt * 256; };
+    auto kstart = [&](int tile) { return (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
         if (lane == 0) {
-            int issued[S];                                // per stage: loads issued so far
+            // ---- TMA producers: X' (warp 0), weights (warp 2)
+            const bool xs = warp == 0;
+            RingPos<kXStages> px;
+            RingPos<kWStages> pw;
+            uint32_t issued[kWStages];                    // loads issued so far per slot (for the drain)
 #pragma unroll
-            for (int s = 0; s < S; ++s) issued[s] = 0;
-            for (int i = 0; i < nk; ++i) {
-                const int s = i % S, u = i / S;
-                if (u > 0 && !mbar_wait(free0 + 8 * s, (u - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort)) break;
-                if (*abort) break;
-                const int kb = kstage(i), bar = full0 + 8 * s;
-                mbar_arrive_expect_tx(bar, kPairX + kPairW + 8 * 32 * a.gs + kPairZ);
-                tma_load_2d(sX + s * kPairX, &tm_x, kb * 128, n0 + 128 * rank, bar);
-                tma_load_2d(sX + s * kPairX + kHalfX, &tm_x, kb * 128 + 64, n0 + 128 * rank, bar);
-                tma_load_2d(sW + s * kPairW, &tm_w, kb * 256, rb0, bar);
-                tma_load_2d(sS + s * kPairS, &tm_s, kb * 8 * a.gs, rb0, bar);
-                tma_load_2d(sZ + s * kPairZ, &tm_z, (a.gs == 2 ? kb : kb >> 1) * 16, rb0, bar);
+            for (int s = 0; s < kWStages; ++s) issued[s] = 0;
+            bool ok = true;
+            for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
+                const int rb0 = row_block0(tile), n0 = token0(tile) + 128 * (int)rank;
+                int kb = kstart(tile);
+                for (int i = 0; i < nk; ++i) {
+                    const int slot = xs ? px.slot : pw.slot;
+                    const uint32_t use = xs ? px.use : pw.use;
+                    ok = (use == 0 || mbar_wait((xs ? free0 : wfree0) + 8 * slot, (use - 1) & 1,
+                                                kFaultGemmPair + kFaultTmaWait, abort)) && !*abort;
+                    if (!ok) break;
+                    if (xs) {
+                        const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
+                        mbar_arrive_expect_tx(bar, kXStage);
+                        tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
+                        tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
+                        px.next();
+                    } else {
+                        const uint32_t bar = wfull0 + 8 * slot, dst = sW + slot * kWStage;
+                        mbar_arrive_expect_tx(bar, kWCodes + 8 * 32 * a.gs + 128);
+                        tma_load_2d(dst, &tm_w, kb * 256, rb0, bar);
+                        tma_load_2d(dst + kWCodes, &tm_s, kb * 8 * a.gs, rb0, bar);
+                        tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? kb : kb >> 1) * 16, rb0, bar);
+                        pw.next();
+                    }
 #pragma unroll
-                for (int t = 0; t < S; ++t)
-                    if (t == s) issued[t] = u + 1;
-            }
-            int res_issued = 0;
-            if (EPI == kEpiAct && a.has_res)
-                for (int h = 0; h < 2; ++h) {
-                    const int i = nk + h, s = i % S, u = i / S;
-                    if (*abort) break;
-                    if (u > 0 && !mbar_wait(free0 + 8 * s, (u - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort)) break;
-                    mbar_arrive_expect_tx(rfull0 + 8 * h, kPairX);
-                    tma_load_2d(tile_slot(h), &tm_r, rb0 * 16, n0 + 128 * h, rfull0 + 8 * h);
-                    res_issued = h + 1;
+                    for (int t = 0; t < kWStages; ++t)
+                        if (t == slot) issued[t] = use + 1;
+                    kb = kb + 1 == nk ? 0 : kb + 1;
                 }
-            // store the finished tile, 64 tokens at a time
-            const int col0 = EPI == kEpiGated ? rb0 * 8 : rb0 * 16;
-            for (int c = 0; c < 4; ++c) {
-                if (!mbar_wait(ready0 + 8 * c, 0, kFaultGemmPair + kFaultEpilogueWait, abort) || *abort) break;
-                if (col0 < a.width && n0 + 64 * c < a.T) {
-                    tma_store_2d(&tm_y, tile_slot(c >> 1) + (uint32_t)(c & 1) * 64 * kTokenBytes, col0, n0 + 64 * c);
-                    bulk_commit();
-                }
             }
-            bulk_wait_read<0>();
-            if (*abort) {   // drain: every issued load must land before the CTA exits
+            if (*abort)   // drain: every issued load must land before the CTA exits
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (issued[s] > 0) mbar_wait(full0 + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
-                for (int h = 0; h < res_issued; ++h) mbar_wait(rfull0 + 8 * h, 0, kFaultGemmPair + kFaultDrainWait, nullptr);
-            }
+                for (int s = 0; s < kWStages; ++s)
+                    if (issued[s] > 0)
+                        mbar_wait((xs ? xfull0 : wfull0) + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            for (int i = 0; i < nk; ++i) {
-                const int s = i % S, u = i / S;
-                // every warp that reports a stage has seen that CTA's loads of it arrive
-                if (!mbar_wait_cluster(afull0 + 8 * s, u & 1, kFaultGemmPair + kFaultMmaWait, abort)) break;
-                if (!mbar_wait(full0 + 8 * s, u & 1, kFaultGemmPair + kFaultMmaWait, abort)) break;
-                tc_fence_after();
+        if (lane == 0) {
+            RingPos<kXStages> p;
+            uint32_t tiles = 0;
+            bool ok = true;
+            const uint32_t leader_afwd0 = map_to_rank(afwd0, 0);
+            for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters, ++tiles) {
+                // the sums of the tile before are out of tensor memory (the
+                // other CTA's first report of a tile says so for its half)
+                if (tiles > 0) ok = mbar_wait(accfree, (tiles - 1) & 1, kFaultGemmPair + kFaultMmaWait, abort);
+                for (int i = 0; ok && i < nk; ++i, p.next()) {
+                    const int s = p.slot;
+                    ok = mbar_wait(xfull0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort) &&
+                         mbar_wait(afull0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
+                    if (!ok) break;
+                    if (rank != 0) {
+                        tc_fence_after();
+                        tc_fence_before();
+                        mbar_arrive_other(leader_afwd0 + 8 * s);
+                        continue;
+                    }
+                    ok = mbar_wait_other(afwd0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_f16_ts_pair(tbase, tA + s * 64 + kk * 8,
-                                     umma_desc_sw128_kmajor(sX + s * kPairX + (kk >> 2) * kHalfX) + (uint64_t)((kk & 3) * 2),
-                                     kIdesc, i + kk > 0 ? 1u : 0u);
-                umma_commit_pair(free0 + 8 * s);
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_f16_ts_pair(tbase, tA + s * 64 + kk * 8,
+                                         umma_desc_sw128_kmajor(sX + s * kXStage + (kk >> 2) * kHalfX) + (uint64_t)((kk & 3) * 2),
+                                         kIdesc, i + kk > 0 ? 1u : 0u);
+                    umma_commit_pair(free0 + 8 * s);
+                }
+                if (rank == 0 && ok) umma_commit_pair(accfull);
             }
-            umma_commit_pair(done);                       // always: arrives once every MMA issued above has completed
-        } else if (lane == 0) {
-            // the other CTA reports a stage once, for its eight warps: a
-            // cluster-scope release by each of them cost 900 cycles a stage
-            const uint32_t leader_afull0 = map_to_rank(afull0, 0);
-            for (int i = 0; i < nk; ++i) {
-                const int s = i % S, u = i / S;
-                if (!mbar_wait(afull0 + 8 * s, u & 1, kFaultGemmPair + kFaultMmaWait, abort)) break;
-                mbar_arrive_cluster(leader_afull0 + 8 * s);
+            if (rank == 0) umma_commit_pair(fin);         // always: arrives once every MMA issued above has completed
+        }
+    } else if (warp < 11) {
+        // ---- dequantisation
+        const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
+        const int half = (warp - 3) >> 2;                 // channels 64 half .. + 63 of a stage
+        const int g = lane >> 2;
+        RingPos<kXStages> p;
+        RingPos<kWStages> pw;
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
+            int kb = kstart(tile);
+            for (int i = 0; i < nk; ++i, p.next(), pw.next()) {
+                const int s = p.slot;
+                // the tensor-memory stores below are warp-collective: the whole
+                // warp goes on only if every lane saw the stage arrive
+                ok = mbar_wait(wfull0 + 8 * pw.slot, pw.use & 1, kFaultGemmPair + kFaultDequantWait, abort) && !*abort;
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint32_t src = sW + pw.slot * kWStage, zsel = a.gs == 2 ? half : kb & 1;
+                uint4 wv[2];
+                uint32_t sw[2], zb[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int rbl = 2 * qw + r;
+                    wv[r] = lds128(src + rbl * 1024 + half * 512 + lane * 16);
+                    sw[r] = lds32(src + kWCodes + (rbl * a.gs + (a.gs == 2 ? half : 0)) * 32 + g * 4);
+                    zb[r] = lds8(src + kWCodes + kWScales + rbl * 16 + zsel * 8 + g);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wfree0 + 8 * pw.slot);
+                ok = p.use == 0 || mbar_wait(free0 + 8 * s, (p.use - 1) & 1, kFaultGemmPair + kFaultDequantWait, abort);
+                if (!__all_sync(0xffffffffu, ok && !*abort)) { ok = false; break; }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t sc0, sc1, regs[16];
+                    scale_pairs(sw[r], sc0, sc1);
+                    const Zero2 zc = zero_consts(zb[r]);
+                    dequant_word(wv[r].x, zc, sc0, sc1, regs + 0);
+                    dequant_word(wv[r].y, zc, sc0, sc1, regs + 4);
+                    dequant_word(wv[r].z, zc, sc0, sc1, regs + 8);
+                    dequant_word(wv[r].w, zc, sc0, sc1, regs + 12);
+                    tmem_st_16x256b_x4(tA + s * 64 + half * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(afull0 + 8 * s);
+                kb = kb + 1 == nk ? 0 : kb + 1;
             }
         }
     } else {
-        const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
-        const int half = (warp - 2) >> 2;                 // channels 64 half .. of a stage, then tokens 128 half ..
-        const int g = lane >> 2;
-        for (int i = 0; i < nk; ++i) {
-            const int s = i % S, u = i / S;
-            // the tensor-memory stores below are warp-collective: the whole
-            // warp goes on only if every lane saw the stage arrive
-            if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, u & 1, kFaultGemmPair + kFaultDequantWait, abort) && !*abort))
-                break;
-            const uint32_t zsel = a.gs == 2 ? half : kstage(i) & 1;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int rbl = 2 * qw + r;
-                const uint4 wv = lds128(sW + s * kPairW + rbl * 1024 + half * 512 + lane * 16);
-                uint32_t sc0, sc1, regs[16];
-                scale_pairs(lds32(sS + s * kPairS + (rbl * a.gs + (a.gs == 2 ? half : 0)) * 32 + g * 4), sc0, sc1);
-                const Zero2 zc = zero_consts(lds8(sZ + s * kPairZ + rbl * 16 + zsel * 8 + g));
-                dequant_word(wv.x, zc, sc0, sc1, regs + 0);
-                dequant_word(wv.y, zc, sc0, sc1, regs + 4);
-                dequant_word(wv.z, zc, sc0, sc1, regs + 8);
-                dequant_word(wv.w, zc, sc0, sc1, regs + 12);
-                tmem_st_16x256b_x4(tA + s * 64 + half * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(afull0 + 8 * s);
-        }
-
         // ---- epilogue: one accumulator row per thread, tokens 128 half .. + 127
-        // (skipped after an abort: the tile is not valid, and the fault word says so)
-        bool ok = mbar_wait(done, 0, kFaultGemmPair + kFaultEpilogueWait, abort);
-        if (ok && EPI == kEpiAct && a.has_res)
-            ok = mbar_wait(rfull0 + 8 * half, 0, kFaultGemmPair + kFaultEpilogueWait, abort);
-        if (__all_sync(0xffffffffu, ok && !*abort)) {
+        const int qw = warp & 3, half = (warp - 11) >> 2, ew = warp - 11;
+        const bool up = EPI == kEpiGated && (lane & 8);
+        const int ch = EPI == kEpiGated ? (lane >> 4) * 8 + (lane & 7) : lane;         // channel in the warp's buffer
+        const uint32_t buf0 = sOut + (uint32_t)ew * 2 * kOutBuf, rbar0 = rfull0 + 16 * ew;
+        const bool res = EPI == kEpiAct && a.has_res;
+        uint32_t tiles = 0, loads[2] = {0, 0};            // residual loads issued into each buffer
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters, ++tiles) {
+            const int rb0 = row_block0(tile) + 2 * qw, t0 = token0(tile) + 128 * half;
+            const int col0 = EPI == kEpiGated ? rb0 * 8 : rb0 * 16;
+            const int row = rb0 * 16 + lane;
+            const bool in_row = col0 < a.width;           // of the whole warp (a warp's rows are two row blocks)
+            float b = 0.f;
+            if (a.bias && row < a.out) b = __half2float(a.bias[EPI == kEpiGated ? col0 + ch + (up ? a.width : 0) : row]);
+            // batch j: tokens t0 + 32 j .. + 31, buffer j & 1
+            auto live = [&](int j) { return in_row && t0 + 32 * j < a.T; };
+            auto load_residual = [&](int j) {             // lane 0, once the buffer's last store has been read
+                mbar_arrive_expect_tx(rbar0 + 8 * (j & 1), kOutBuf);
+                tma_load_2d(buf0 + (j & 1) * kOutBuf, &tm_r, col0, t0 + 32 * j, rbar0 + 8 * (j & 1));
+            };
+            if (lane == 0) bulk_wait_read<0>();           // the last tile's stores have read both buffers
+            if (res) {                                    // the first two batches' residual, ahead of the sums
+                if (lane == 0)
+                    for (int j = 0; j < 2; ++j)
+                        if (live(j)) load_residual(j);
+                for (int j = 0; j < 2; ++j)
+                    if (live(j)) ++loads[j];
+            }
+            ok = mbar_wait(accfull, tiles & 1, kFaultGemmPair + kFaultEpilogueWait, abort) && !*abort;
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            const int rloc = 32 * qw + lane, row = rb0 * 16 + rloc;
-            const bool up = EPI == kEpiGated && (lane & 8);
-            const int ch = EPI == kEpiGated ? (rloc >> 4) * 8 + (lane & 7) : rloc;      // channel of the tile
-            const int bias_at = EPI == kEpiGated ? rb0 * 8 + ch + (up ? a.width : 0) : row;
-            const float b = a.bias && row < a.out ? __half2float(a.bias[bias_at]) : 0.f;
-            const uint32_t at = tile_slot(half) + (uint32_t)ch * 2;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {                 // 32 tokens
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * qw) << 16) + half * 128 + c * 32, r);
+            for (int q = 0; q < 2; ++q) {                 // 64 tokens
+                uint32_t r[64];
+                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * qw) << 16) + half * 128 + q * 64, r);
+                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * qw) << 16) + half * 128 + q * 64 + 32, r + 32);
                 tmem_wait_ld();
-                const uint32_t to = at + (uint32_t)c * 32 * kTokenBytes;
-                if (EPI == kEpiGated) with_act(a.act, PairGated{r, b, to, up});
-                else with_act(a.act, PairAct{r, b, to, a.has_res != 0});
-                if (c & 1) {                              // 64 tokens of this quarter of the rows are written
+                if (q == 1) {                             // every sum is in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(accfree);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 2 * q + h;
+                    if (!live(j)) continue;
+                    if (res) {
+                        ok = mbar_wait(rbar0 + 8 * h, (loads[h] - 1) & 1, kFaultGemmPair + kFaultEpilogueWait, abort);
+                        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    } else {
+                        if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has been read
+                        __syncwarp();
+                    }
+                    const uint32_t at = buf0 + h * kOutBuf + (uint32_t)ch * 2 + (up ? kTokenBytes : 0);
+                    if (EPI == kEpiGated) with_act(a.act, PairGated{r + 32 * h, b, at, up});
+                    else with_act(a.act, PairAct{r + 32 * h, b, at, res});
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(ready0 + 8 * (2 * half + (c >> 1)));
+                    if (lane == 0) {
+                        tma_store_2d(&tm_y, buf0 + h * kOutBuf, col0, t0 + 32 * j);
+                        bulk_commit();
+                    }
+                    if (res && j + 2 < 4 && live(j + 2)) {
+                        if (lane == 0) {
+                            bulk_wait_read<0>();
+                            load_residual(j + 2);
+                        }
+                        ++loads[h];
+                    }
                 }
+                if (!ok) break;
             }
         }
+        if (lane == 0) bulk_wait_read<0>();               // stores have read their buffers before the CTA exits
+        if (*abort && lane == 0)
+            for (int h = 0; h < 2; ++h)
+                if (loads[h] > 0) mbar_wait(rbar0 + 8 * h, (loads[h] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_arrive_wait();                                // neither CTA leaves while the other may still signal it
     if (warp == 1) {
         // no MMA may still write tensor memory when it is released
-        mbar_wait(done, 0, kFaultGemmPair + kFaultDrainWait, nullptr);
+        mbar_wait(fin, 0, kFaultGemmPair + kFaultDrainWait, nullptr);
         tc_fence_after();
         tmem_dealloc_pair(tbase, 512);
     }
@@ -380,36 +490,43 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 
 namespace {
 
+// Launch on as many clusters as can be resident (74 on 148 SMs), at most one per tile.
 template <int EPI>
-cudaError_t launch_pair(const CUtensorMap* tm, const PairArgs& a, int mt, int nt, cudaStream_t s) {
-    // kernel attributes, set once per device (double-checked under a lock)
-    static std::atomic<bool> configured[64] = {};
+cudaError_t launch_pair(const CUtensorMap* tm, const PairArgs& a, cudaStream_t s) {
+    // kernel attributes and residency, once per device (double-checked under a lock)
+    static std::atomic<int> resident[64] = {};
     static std::mutex mu;
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!configured[dev].load(std::memory_order_relaxed)) {
-            const cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<EPI>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
-            if (e != cudaSuccess) return e;
-            configured[dev].store(true, std::memory_order_release);
-        }
-    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(mt, nt, 1);
+    cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = resident[dev].load(std::memory_order_acquire);
+    if (clusters == 0) {
+        std::lock_guard<std::mutex> lock(mu);
+        clusters = resident[dev].load(std::memory_order_relaxed);
+        if (clusters == 0) {
+            cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)kPairSmem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, gemm_pair_kernel<EPI>, &cfg);
+            if (e != cudaSuccess) return e;
+            if (clusters < 1) return cudaErrorLaunchOutOfResources;
+            resident[dev].store(clusters, std::memory_order_release);
+        }
+    }
+    cfg.gridDim = dim3(2 * (unsigned)std::min(clusters, a.ntiles), 1, 1);
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<EPI>, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
 }
@@ -419,9 +536,8 @@ cudaError_t launch_pair(const CUtensorMap* tm, const PairArgs& a, int mt, int nt
 // Tensor maps: X' fp16 [T][in], box 64 channels x 128 tokens, 128-byte
 // swizzle; codes as uint32 [out/16][in/128 * 256], box 128 channels x 8 row
 // blocks; scales uint32 [out/16][G * 8], box the stage's groups x 8 row
-// blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y fp16
-// [T][width], box 128 (gated: 64) columns x 64 tokens; residual fp16 [T][out],
-// box 128 columns x 128 tokens. Rows past T or out are read as zeros and not
+// blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y and
+// the residual fp16 [T][width], box 32 (gated: 16) columns x 32 tokens. Rows past T or out are read as zeros and not
 // written.
 cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
                              int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, const Epilogue& epi) {
@@ -448,12 +564,13 @@ cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, co
                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
         encode_tma_2d(&tm[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, zp, Gp * 8, nrb, Gp * 8, 16u, 8u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
         encode_tma_2d(&tm[4], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Y, (uint64_t)a.width, (uint64_t)T, (uint64_t)a.width * 2,
-                      gated ? 64u : 128u, 64u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+                      gated ? 16u : 32u, 32u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
         encode_tma_2d(&tm[5], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, epi.residual ? epi.residual : Y, (uint64_t)a.width,
-                      (uint64_t)T, (uint64_t)a.width * 2, gated ? 64u : 128u, 128u, CU_TENSOR_MAP_SWIZZLE_NONE);
+                      (uint64_t)T, (uint64_t)a.width * 2, gated ? 16u : 32u, 32u, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) return cudaErrorInvalidValue;
-    const int mt = 2 * (int)((nrb + 15) / 16), nt = (int)((T + 255) / 256);
-    const cudaError_t e = gated ? launch_pair<kEpiGated>(tm, a, mt, nt, s) : launch_pair<kEpiAct>(tm, a, mt, nt, s);
+    a.mt = (int)((nrb + 15) / 16);
+    a.ntiles = a.mt * (int)((T + 255) / 256);
+    const cudaError_t e = gated ? launch_pair<kEpiGated>(tm, a, s) : launch_pair<kEpiAct>(tm, a, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
