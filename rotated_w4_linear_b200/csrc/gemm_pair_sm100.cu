@@ -8,20 +8,18 @@
 // a cluster walks the tiles cid, cid + clusters, ... (row tiles first, so that
 // the clusters at work share their tokens), and its roles run ahead of each
 // other across tiles. Per CTA, nineteen warps:
-//   warp 0      TMA producer of X': per stage of 128 channels the CTA's 128
-//               tokens (two 64-channel boxes, 128-byte swizzle), ring of 4;
-//   warp 2      TMA producer of the weights: the stage's int4 codes of 8 row
-//               blocks with their scales and zeros, ring of 6: they are small,
-//               so they run further ahead than X', and the dequantisation of
-//               a stage does not wait behind its X' load;
+//   warp 0      TMA producer: per stage of 128 channels the CTA's 128 tokens
+//               of X' (two 64-channel boxes, 128-byte swizzle; ring of 4) and,
+//               two stages ahead of it, the int4 codes of its 8 row blocks with
+//               their scales and zeros (ring of 6);
 //   warps 3-10  dequantise (w_hat = fp16((q - z) s), as the other kernels do)
 //               into a ring of 4 tensor-memory stages: a warp takes one
 //               quarter of the rows and one half of the stage's channels;
+//   warp 2      gate: one lane reports to the leader CTA when its CTA's X' and
+//               w_hat of a stage are there;
 //   warp 1      tensor memory; in the leader CTA one lane issues the MMAs
-//               (A from tensor memory, B from shared memory) once its
-//               dequantisation warps and the other CTA have reported the
-//               stage, and commits it back to both CTAs; in the other CTA one
-//               lane forwards its CTA's reports;
+//               (A from tensor memory, B from shared memory) of a stage that
+//               both gates have reported, and commits it back to both CTAs;
 //   warps 11-18 epilogue: a warp takes one quarter of the rows and one half of
 //               the tokens, 64 tokens at a time from tensor memory into
 //               registers (after the second 64 the accumulator is free for
@@ -134,6 +132,12 @@ __device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tme
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // Arrive on `bar` of both CTAs once every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
     asm volatile(
@@ -216,7 +220,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     const uint32_t sX = smem_addr(smem), sOut = sX + kXStages * kXStage, sW = sOut + 16 * kOutBuf;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)kXStages * kXStage + 16 * kOutBuf + (size_t)kWStages * kWStage);
     const uint32_t xfull0 = smem_addr(bars), free0 = xfull0 + 8 * kXStages, afull0 = free0 + 8 * kXStages;
-    const uint32_t afwd0 = afull0 + 8 * kXStages, wfull0 = afwd0 + 8 * kXStages, wfree0 = wfull0 + 8 * kWStages;
+    const uint32_t go0 = afull0 + 8 * kXStages, wfull0 = go0 + 8 * kXStages, wfree0 = wfull0 + 8 * kWStages;
     const uint32_t accfull = wfree0 + 8 * kWStages, accfree = accfull + 8, fin = accfree + 8, rfull0 = fin + 8;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 4 * kXStages + 2 * kWStages + 8 + 16);
     volatile uint32_t* abort = tslot + 1;
@@ -231,7 +235,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             mbar_init(xfull0 + 8 * s, 1);
             mbar_init(free0 + 8 * s, 1);                  // the MMAs on X' stage and w_hat stage s are done
             mbar_init(afull0 + 8 * s, 8);                 // this CTA's dequantisation warps
-            mbar_init(afwd0 + 8 * s, 1);                  // leader: the other CTA's report
+            mbar_init(go0 + 8 * s, 2);                    // leader: both CTAs' gates
         }
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull0 + 8 * s, 1);
@@ -268,85 +272,123 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     auto token0 = [&](int tile) { return tile / a.mt * 256; };
     auto kstart = [&](int tile) { return (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
 
-    if (warp == 0 || warp == 2) {
+    if (warp == 0) {
         if (lane == 0) {
-            // ---- TMA producers: X' (warp 0), weights (warp 2)
-            const bool xs = warp == 0;
+            // ---- TMA producer: the weights of a stage go out two stages
+            // before its X', so they never wait behind an X' slot
+            constexpr int kAhead = kWStages - kXStages;
             RingPos<kXStages> px;
             RingPos<kWStages> pw;
-            uint32_t issued[kWStages];                    // loads issued so far per slot (for the drain)
+            uint32_t xissued[kXStages], wissued[kWStages];    // loads issued so far per slot (for the drain)
 #pragma unroll
-            for (int s = 0; s < kWStages; ++s) issued[s] = 0;
+            for (int s = 0; s < kXStages; ++s) xissued[s] = 0;
+#pragma unroll
+            for (int s = 0; s < kWStages; ++s) wissued[s] = 0;
+            int wtile = first_tile, wi = 0, wkb = wtile < a.ntiles ? kstart(wtile) : 0;
+            auto issue_w = [&]() {                        // the next stage's weights, if there is one
+                if (wtile >= a.ntiles) return true;
+                if (pw.use > 0 && !mbar_wait(wfree0 + 8 * pw.slot, (pw.use - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort))
+                    return false;
+                const int rb0 = row_block0(wtile);
+                const uint32_t bar = wfull0 + 8 * pw.slot, dst = sW + pw.slot * kWStage;
+                mbar_arrive_expect_tx(bar, kWCodes + 8 * 32 * a.gs + 128);
+                tma_load_2d(dst, &tm_w, wkb * 256, rb0, bar);
+                tma_load_2d(dst + kWCodes, &tm_s, wkb * 8 * a.gs, rb0, bar);
+                tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? wkb : wkb >> 1) * 16, rb0, bar);
+#pragma unroll
+                for (int t = 0; t < kWStages; ++t)
+                    if (t == pw.slot) wissued[t] = pw.use + 1;
+                pw.next();
+                wkb = wkb + 1 == nk ? 0 : wkb + 1;
+                if (++wi == nk) {
+                    wi = 0;
+                    wtile += nclusters;
+                    if (wtile < a.ntiles) wkb = kstart(wtile);
+                }
+                return true;
+            };
             bool ok = true;
+            for (int i = 0; ok && i < kAhead; ++i) ok = issue_w();
             for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
-                const int rb0 = row_block0(tile), n0 = token0(tile) + 128 * (int)rank;
+                const int n0 = token0(tile) + 128 * (int)rank;
                 int kb = kstart(tile);
                 for (int i = 0; i < nk; ++i) {
-                    const int slot = xs ? px.slot : pw.slot;
-                    const uint32_t use = xs ? px.use : pw.use;
-                    ok = (use == 0 || mbar_wait((xs ? free0 : wfree0) + 8 * slot, (use - 1) & 1,
-                                                kFaultGemmPair + kFaultTmaWait, abort)) && !*abort;
+                    ok = issue_w() && (px.use == 0 || mbar_wait(free0 + 8 * px.slot, (px.use - 1) & 1,
+                                                                kFaultGemmPair + kFaultTmaWait, abort)) && !*abort;
                     if (!ok) break;
-                    if (xs) {
-                        const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
-                        mbar_arrive_expect_tx(bar, kXStage);
-                        tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
-                        tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
-                        px.next();
-                    } else {
-                        const uint32_t bar = wfull0 + 8 * slot, dst = sW + slot * kWStage;
-                        mbar_arrive_expect_tx(bar, kWCodes + 8 * 32 * a.gs + 128);
-                        tma_load_2d(dst, &tm_w, kb * 256, rb0, bar);
-                        tma_load_2d(dst + kWCodes, &tm_s, kb * 8 * a.gs, rb0, bar);
-                        tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? kb : kb >> 1) * 16, rb0, bar);
-                        pw.next();
-                    }
+                    const uint32_t bar = xfull0 + 8 * px.slot, dst = sX + px.slot * kXStage;
+                    mbar_arrive_expect_tx(bar, kXStage);
+                    tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
+                    tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
 #pragma unroll
-                    for (int t = 0; t < kWStages; ++t)
-                        if (t == slot) issued[t] = use + 1;
+                    for (int t = 0; t < kXStages; ++t)
+                        if (t == px.slot) xissued[t] = px.use + 1;
+                    px.next();
                     kb = kb + 1 == nk ? 0 : kb + 1;
                 }
             }
-            if (*abort)   // drain: every issued load must land before the CTA exits
+            if (*abort) {   // drain: every issued load must land before the CTA exits
+#pragma unroll
+                for (int s = 0; s < kXStages; ++s)
+                    if (xissued[s] > 0) mbar_wait(xfull0 + 8 * s, (xissued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
 #pragma unroll
                 for (int s = 0; s < kWStages; ++s)
-                    if (issued[s] > 0)
-                        mbar_wait((xs ? xfull0 : wfull0) + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
+                    if (wissued[s] > 0) mbar_wait(wfull0 + 8 * s, (wissued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
+            }
         }
-    } else if (warp == 1) {
+    } else if (warp == 2) {
         if (lane == 0) {
+            // ---- gate: one report per stage to the leader's MMA thread, which
+            // then looks at a single barrier (a look takes about 100 cycles,
+            // and its MMA queue does not hold enough work for three)
+            const uint32_t go_leader0 = map_to_rank(go0, 0);
             RingPos<kXStages> p;
             uint32_t tiles = 0;
             bool ok = true;
-            const uint32_t leader_afwd0 = map_to_rank(afwd0, 0);
             for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters, ++tiles) {
-                // the sums of the tile before are out of tensor memory (the
-                // other CTA's first report of a tile says so for its half)
+                // the sums of the tile before are out of this CTA's tensor memory
                 if (tiles > 0) ok = mbar_wait(accfree, (tiles - 1) & 1, kFaultGemmPair + kFaultMmaWait, abort);
                 for (int i = 0; ok && i < nk; ++i, p.next()) {
-                    const int s = p.slot;
-                    ok = mbar_wait(xfull0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort) &&
-                         mbar_wait(afull0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
-                    if (!ok) break;
-                    if (rank != 0) {
-                        tc_fence_after();
-                        tc_fence_before();
-                        mbar_arrive_other(leader_afwd0 + 8 * s);
-                        continue;
-                    }
-                    ok = mbar_wait_other(afwd0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
+                    ok = mbar_wait(xfull0 + 8 * p.slot, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort) &&
+                         mbar_wait(afull0 + 8 * p.slot, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_f16_ts_pair(tbase, tA + s * 64 + kk * 8,
-                                         umma_desc_sw128_kmajor(sX + s * kXStage + (kk >> 2) * kHalfX) + (uint64_t)((kk & 3) * 2),
-                                         kIdesc, i + kk > 0 ? 1u : 0u);
-                    umma_commit_pair(free0 + 8 * s);
+                    tc_fence_before();
+                    mbar_arrive_other(go_leader0 + 8 * p.slot);
                 }
-                if (rank == 0 && ok) umma_commit_pair(accfull);
             }
-            if (rank == 0) umma_commit_pair(fin);         // always: arrives once every MMA issued above has completed
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---- MMA issuer. The whole warp walks the stages, so that the
+            // operands' addresses stay in uniform registers, and one elected
+            // lane issues (with the loop inside a one-lane branch the eight
+            // MMAs of a stage took 550 cycles to issue, and the tensor cores
+            // idled a fifth of the time).
+            RingPos<kXStages> p;
+            bool ok = true;
+            for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
+                for (int i = 0; i < nk; ++i, p.next()) {
+                    const int s = p.slot;
+                    ok = __all_sync(0xffffffffu, mbar_wait_other(go0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t b = umma_desc_sw128_kmajor(sX + s * kXStage);
+                    const uint32_t w = tA + s * 64;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)     // two 64-channel boxes of four MMAs each
+                            umma_f16_ts_pair(tbase, w + kk * 8, b + (uint64_t)((kk >> 2) * (kHalfX >> 4) + (kk & 3) * 2), kIdesc,
+                                             i + kk > 0 ? 1u : 0u);
+                        umma_commit_pair(free0 + 8 * s);
+                    }
+                    __syncwarp();
+                }
+                if (ok && elect_one()) umma_commit_pair(accfull);
+                __syncwarp();
+            }
+            if (elect_one()) umma_commit_pair(fin);       // always: arrives once every MMA issued above has completed
+            __syncwarp();
         }
     } else if (warp < 11) {
         // ---- dequantisation
