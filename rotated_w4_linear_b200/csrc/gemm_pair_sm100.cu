@@ -1,40 +1,50 @@
-// Prefill contraction on pairs of SMs (tcgen05, cta_group::2), for the layer
-// with an activation and a residual and for the gated up-projection:
-//   Y^T tile [256 rows][256 tokens] = w_hat * X'^T, then the epilogue.
+// Contraction on pairs of SMs (tcgen05, cta_group::2) above 16 tokens, for the
+// layer with an activation and a residual and for the gated up-projection:
+//   Y^T tile [256 rows][BN tokens] = w_hat * X'^T, then the epilogue.
 //
 // Two CTAs of a cluster share a tile: each keeps its own 128 rows of w_hat in
 // its tensor memory and holds half of the tokens in shared memory, and one
-// MMA (M = 256, N = 256, K = 16) reads both halves. The kernel is persistent:
-// a cluster walks the tiles cid, cid + clusters, ... (row tiles first, so that
-// the clusters at work share their tokens), and its roles run ahead of each
-// other across tiles. Per CTA, nineteen warps:
-//   warp 0      TMA producer: per stage of 128 channels the CTA's 128 tokens
-//               of X' (two 64-channel boxes, 128-byte swizzle; ring of 4) and,
-//               two stages ahead of it, the int4 codes of its 8 row blocks with
-//               their scales and zeros (ring of 6);
+// MMA (M = 256, N = BN, K = 16) reads both halves. Two forms:
+//   BN = 256 (above 128 tokens; bound by the tensor cores and their power):
+//     persistent; a cluster of one pair walks the tiles cid, cid + clusters,
+//     ... (row tiles first, so that the clusters at work share their tokens)
+//     and its roles run ahead of each other across tiles;
+//   BN = 64, 128 (17 to 128 tokens; bound by the weights' way to the tensor
+//     cores): one tile per cluster, whose 1, 2 or 4 pairs split the channels,
+//     since the row tiles alone would leave most SMs idle; the pairs' sums
+//     meet through distributed shared memory in a fixed order.
+// Per CTA, nineteen warps:
+//   warp 0      TMA producer: per stage of 128 channels the CTA's half of the
+//               tokens of X' (two 64-channel boxes, 128-byte swizzle) and, two
+//               stages ahead of it, the int4 codes of its 8 row blocks with
+//               their scales and zeros;
 //   warps 3-10  dequantise (w_hat = fp16((q - z) s), as the other kernels do)
-//               into a ring of 4 tensor-memory stages: a warp takes one
-//               quarter of the rows and one half of the stage's channels;
-//   warp 2      gate: one lane reports to the leader CTA when its CTA's X' and
-//               w_hat of a stage are there;
-//   warp 1      tensor memory; in the leader CTA one lane issues the MMAs
-//               (A from tensor memory, B from shared memory) of a stage that
-//               both gates have reported, and commits it back to both CTAs;
-//   warps 11-18 epilogue: a warp takes one quarter of the rows and one half of
-//               the tokens, 64 tokens at a time from tensor memory into
-//               registers (after the second 64 the accumulator is free for
-//               the next tile), then through a 32-token buffer of its own in
-//               shared memory, where the residual has arrived by TMA, to a TMA
-//               store.
-// Tensor memory: 256 columns of fp32 sums, 4 x 64 columns of w_hat (all 512),
-// so there is one accumulator: the MMAs pause from a tile's last commit until
-// its sums are in registers.
+//               into a ring of tensor-memory stages: a warp takes one quarter
+//               of the rows and one half of the stage's channels;
+//   warp 2      gate: one lane reports to the pair's leader when its CTA's X'
+//               and w_hat of a stage are there;
+//   warp 1      tensor memory; in the leader the warp issues the MMAs (A from
+//               tensor memory, B from shared memory) of a stage that both
+//               gates have reported, and commits it back to both CTAs;
+//   warps 11-18 epilogue, BN = 256: a warp takes one quarter of the rows and
+//               one half of the tokens, 64 tokens at a time from tensor memory
+//               into registers (after the second 64 the accumulator is free
+//               for the next tile), then through a 32-token buffer of its own
+//               in shared memory, where the residual has arrived by TMA, to a
+//               TMA store. BN < 256: the warps put the fp32 sums into shared
+//               memory (the rings' space), and after a cluster barrier all
+//               warps add the pairs' sums, apply the epilogue and store.
 // All waits are bounded (sm100.cuh); a wait that runs out raises the CTA's
-// abort flag, every role stops, what was issued is drained, and both CTAs meet
-// at the last cluster barrier.
+// abort flag, every role stops, what was issued is drained, and the cluster's
+// CTAs meet at the last barrier.
 //
-// A token's result does not depend on its place in the batch: the order of
-// the channels goes by the row tile alone.
+// What it does per stage (128 rows x 128 channels x 256 tokens per CTA, SM
+// cycles, 4096 -> 28672): the tensor cores need 1024, the kernel takes 1191;
+// with a cluster-scope release by each dequantisation warp it took 1766, with
+// the MMAs issued from a one-lane branch 1246.
+//
+// With BN = 256 a token's result does not depend on its place in the batch:
+// the order of the channels goes by the row tile alone.
 #include <cuda.h>
 
 #include <algorithm>
@@ -50,24 +60,42 @@ namespace paro {
 
 namespace {
 
-constexpr int kXStages = 4, kWStages = 6;
 constexpr int kPairThreads = 608;
-constexpr uint32_t kHalfX = 128 * 128;                  // 128 tokens x 64 channels
-constexpr uint32_t kXStage = 2 * kHalfX;                // 32 KB: 128 tokens x 128 channels
 constexpr uint32_t kWCodes = 8 * 1024;                  // 8 row blocks x 128 channels of codes
 constexpr uint32_t kWScales = 8 * 64;                   // 8 row blocks x up to 2 groups x 8 words
 constexpr uint32_t kWStage = kWCodes + kWScales + 128;  // zeros: 8 row blocks x 2 groups x 8 bytes
 constexpr uint32_t kOutBuf = 32 * 64;                   // 32 tokens x 32 rows of fp16: two for each epilogue warp
-constexpr uint32_t kPairBars = 8 * (4 * kXStages + 2 * kWStages + 8 + 16) + 16;
-constexpr size_t kPairSmem = 1024 + (size_t)kXStages * kXStage + (size_t)kWStages * kWStage + 16 * kOutBuf + kPairBars;
+
+// Rings and shared memory for a tile of BN tokens. Tensor memory: BN columns
+// of fp32 sums, 64 columns per w_hat stage (as many stages as fit 512
+// columns, and no more than the ring of X').
+template <int BN>
+struct PairCfg {
+    static constexpr bool kSplit = BN < 256;
+    static constexpr int kXStages = kSplit ? 6 : 4, kWStages = kXStages + 2;
+    static constexpr uint32_t kHalfX = BN / 2 * 128;    // BN / 2 tokens x 64 channels
+    static constexpr uint32_t kXStage = 2 * kHalfX;
+    static constexpr uint32_t kOut = kSplit ? 0 : 16 * kOutBuf;
+    static constexpr uint32_t kRings = kXStages * kXStage + kOut + kWStages * kWStage;
+    static constexpr uint32_t kSums = kSplit ? BN * 128 * 4 : 0;       // in the rings' space
+    static constexpr uint32_t kBody = kRings > kSums ? kRings : kSums;
+    static constexpr int kBars = 4 * kXStages + 2 * kWStages + 3 + 16;
+    static constexpr size_t kSmem = 1024 + (size_t)kBody + 8 * kBars + 16;
+    static_assert(BN + 64 * kXStages <= 512, "tensor memory");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+constexpr int kMaxPairs = 4;                            // pairs that may split a tile's channels (cluster of 8)
 
 struct PairArgs {
     int T, out, nk;             // nk: 128-channel stages
     int mt, ntiles;             // 256-row tiles; tiles in all
+    int pairs;                  // pairs per cluster (BN < 256: they split the channels)
     int width;                  // columns of Y (out, or out / 2 for the gated epilogue)
     int gs;                     // quantisation groups per 128 channels (1, or 2 for group 64)
     int act, has_res;
     const __half* bias;
+    const __half* residual;     // BN < 256: read with plain loads
+    __half* Y;                  // BN < 256: written with plain stores
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -138,11 +166,17 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// Arrive on `bar` of both CTAs once every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+// Arrive on `bar` of the CTAs in `mask` once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(bar), "h"((uint16_t)3) : "memory");
+        ::"r"(bar), "h"(mask) : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, float v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__half_as_ushort(__float2half_rn(v))) : "memory");
@@ -189,6 +223,65 @@ struct PairGated {
     }
 };
 
+// BN < 256: the pairs' sums of this CTA's rows, added in pair order, to the
+// output: tokens [BN pair / pairs, BN (pair + 1) / pairs), four rows (gated:
+// four gate and four up rows) of one token per thread and step. A CTA whose
+// rows or tokens lie outside takes no part.
+template <int BN, int EPI>
+__device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums, int rb0, uint32_t rank, int pair,
+                                               int pairs) {
+    constexpr int kFours = EPI == kEpiGated ? 16 : 32;     // fours per token
+    const int t0 = BN * pair / pairs, t1 = min(a.T, BN * (pair + 1) / pairs);
+    const int c0 = EPI == kEpiGated ? rb0 * 8 : rb0 * 16;
+    for (int i = threadIdx.x; i < (t1 - t0) * kFours; i += kPairThreads) {
+        const int t = t0 + i / kFours, k = i % kFours;
+        // gated: the k-th four gate rows sit in row block k / 2, their up rows eight further on
+        const int r = EPI == kEpiGated ? (k >> 1) * 16 + (k & 1) * 4 : 4 * k;
+        const int c = c0 + 4 * k;
+        if (c >= a.width) continue;
+        const uint32_t at = sums + (uint32_t)(t * 128 + r) * 4;
+        float4 v[kMaxPairs], u[kMaxPairs];
+#pragma unroll
+        for (int x = 0; x < kMaxPairs; ++x)
+            if (x < pairs) {
+                const uint32_t from = map_to_rank(at, 2 * x + rank);
+                v[x] = ld_cluster_f4(from);
+                if (EPI == kEpiGated) u[x] = ld_cluster_f4(from + 32);
+            }
+        auto sum = [&](const float4 (&w)[kMaxPairs], int bias_at) {
+            float4 s = w[0];
+#pragma unroll
+            for (int x = 1; x < kMaxPairs; ++x)
+                if (x < pairs) {
+                    s.x += w[x].x;
+                    s.y += w[x].y;
+                    s.z += w[x].z;
+                    s.w += w[x].w;
+                }
+            if (a.bias) {
+                s.x += __half2float(a.bias[bias_at]);
+                s.y += __half2float(a.bias[bias_at + 1]);
+                s.z += __half2float(a.bias[bias_at + 2]);
+                s.w += __half2float(a.bias[bias_at + 3]);
+            }
+            return s;
+        };
+        float4 y = sum(v, c);
+        y = make_float4(act_any(y.x, a.act), act_any(y.y, a.act), act_any(y.z, a.act), act_any(y.w, a.act));
+        const size_t to = (size_t)t * a.width + c;
+        if (EPI == kEpiGated) {
+            const float4 w = sum(u, a.width + c);
+            y = make_float4(y.x * w.x, y.y * w.y, y.z * w.z, y.w * w.w);
+        } else if (a.residual) {
+            const uint2 h = *reinterpret_cast<const uint2*>(a.residual + to);
+            const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+            y = make_float4(y.x + lo.x, y.y + lo.y, y.z + hi.x, y.w + hi.y);
+        }
+        *reinterpret_cast<uint2*>(a.Y + to) = make_uint2(pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+    }
+}
+
 // A ring position: slot and use count of the i-th item, advanced one by one.
 template <int N>
 struct RingPos {
@@ -204,7 +297,7 @@ struct RingPos {
 
 }  // namespace
 
-template <int EPI>
+template <int BN, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                  const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_z,
@@ -213,22 +306,31 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     // the next kernel's CTAs may take SMs as this grid's leave them; it reads
     // nothing of ours before this grid is complete
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr uint32_t kIdesc = umma_idesc_f16(256, 256);
+    using C = PairCfg<BN>;
+    constexpr int kXStages = C::kXStages, kWStages = C::kWStages;
+    constexpr uint32_t kHalfX = C::kHalfX, kXStage = C::kXStage;
+    constexpr uint32_t kIdesc = umma_idesc_f16(256, BN);
     constexpr uint32_t kTokenBytes = EPI == kEpiGated ? 32 : 64;       // one token of an epilogue warp's buffer
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const uint32_t sX = smem_addr(smem), sOut = sX + kXStages * kXStage, sW = sOut + 16 * kOutBuf;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)kXStages * kXStage + 16 * kOutBuf + (size_t)kWStages * kWStage);
+    const uint32_t sX = smem_addr(smem), sOut = sX + kXStages * kXStage, sW = sOut + C::kOut;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBody);
     const uint32_t xfull0 = smem_addr(bars), free0 = xfull0 + 8 * kXStages, afull0 = free0 + 8 * kXStages;
-    const uint32_t go0 = afull0 + 8 * kXStages, wfull0 = go0 + 8 * kXStages, wfree0 = wfull0 + 8 * kWStages;
+    const uint32_t wfull0 = afull0 + 8 * kXStages, wfree0 = wfull0 + 8 * kWStages;
     const uint32_t accfull = wfree0 + 8 * kWStages, accfree = accfull + 8, fin = accfree + 8, rfull0 = fin + 8;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 4 * kXStages + 2 * kWStages + 8 + 16);
+    const uint32_t go0 = rfull0 + 16 * 8;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* abort = tslot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int nclusters = gridDim.x >> 1, nk = a.nk;
-    const int first_tile = blockIdx.x >> 1;
+    const uint32_t crank = cluster_rank(), rank = crank & 1;           // CTA of the cluster, of the pair
+    const uint16_t both = (uint16_t)(3u << (crank & ~1u));             // the pair's CTAs
+    // The channel stages of this pair, walked from a different one in every
+    // row tile, so that concurrent requests spread over the memory channels.
+    const int pair = C::kSplit ? (int)(crank >> 1) : 0, pairs = C::kSplit ? a.pairs : 1;
+    const int k0 = a.nk * pair / pairs, nk = a.nk * (pair + 1) / pairs - k0;
+    const int nclusters = gridDim.x / (2 * pairs);
+    const int first_tile = blockIdx.x / (2 * pairs);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXStages; ++s) {
@@ -260,17 +362,15 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     cluster_arrive_wait();                                // the other CTA's barriers exist too
     tc_fence_after();
     const uint32_t tbase = *tslot;
-    const uint32_t tA = tbase + 256;                      // w_hat stages after the accumulator columns
+    const uint32_t tA = tbase + BN;                       // w_hat stages after the accumulator columns
     // X' is written by the rotation grid launched just before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // tile -> row blocks of this CTA, first token, first channel stage.
-    // Clusters walk the channels from different starting stages, so that
-    // concurrent requests spread over the memory channels; the start goes by
-    // the row tile alone.
+    // tile -> row blocks of this CTA, first token, first channel stage (of k0 .. k0 + nk - 1)
     auto row_block0 = [&](int tile) { return ((tile % a.mt) * 2 + (int)rank) * 8; };
-    auto token0 = [&](int tile) { return tile / a.mt * 256; };
-    auto kstart = [&](int tile) { return (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
+    auto token0 = [&](int tile) { return tile / a.mt * BN; };
+    auto kstart = [&](int tile) { return k0 + (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
+    auto knext = [&](int kb) { return kb + 1 == k0 + nk ? k0 : kb + 1; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -299,7 +399,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 for (int t = 0; t < kWStages; ++t)
                     if (t == pw.slot) wissued[t] = pw.use + 1;
                 pw.next();
-                wkb = wkb + 1 == nk ? 0 : wkb + 1;
+                wkb = knext(wkb);
                 if (++wi == nk) {
                     wi = 0;
                     wtile += nclusters;
@@ -310,7 +410,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             bool ok = true;
             for (int i = 0; ok && i < kAhead; ++i) ok = issue_w();
             for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
-                const int n0 = token0(tile) + 128 * (int)rank;
+                const int n0 = token0(tile) + BN / 2 * (int)rank;
                 int kb = kstart(tile);
                 for (int i = 0; i < nk; ++i) {
                     ok = issue_w() && (px.use == 0 || mbar_wait(free0 + 8 * px.slot, (px.use - 1) & 1,
@@ -324,7 +424,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     for (int t = 0; t < kXStages; ++t)
                         if (t == px.slot) xissued[t] = px.use + 1;
                     px.next();
-                    kb = kb + 1 == nk ? 0 : kb + 1;
+                    kb = knext(kb);
                 }
             }
             if (*abort) {   // drain: every issued load must land before the CTA exits
@@ -341,7 +441,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             // ---- gate: one report per stage to the leader's MMA thread, which
             // then looks at a single barrier (a look takes about 100 cycles,
             // and its MMA queue does not hold enough work for three)
-            const uint32_t go_leader0 = map_to_rank(go0, 0);
+            const uint32_t go_leader0 = map_to_rank(go0, crank & ~1u);
             RingPos<kXStages> p;
             uint32_t tiles = 0;
             bool ok = true;
@@ -378,16 +478,16 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)     // two 64-channel boxes of four MMAs each
-                            umma_f16_ts_pair(tbase, w + kk * 8, b + (uint64_t)((kk >> 2) * (kHalfX >> 4) + (kk & 3) * 2), kIdesc,
+                            umma_f16_ts_pair(tbase, w + kk * 8, b + (uint64_t)((kk >> 2) * (int)(kHalfX >> 4) + (kk & 3) * 2), kIdesc,
                                              i + kk > 0 ? 1u : 0u);
-                        umma_commit_pair(free0 + 8 * s);
+                        umma_commit_pair(free0 + 8 * s, both);
                     }
                     __syncwarp();
                 }
-                if (ok && elect_one()) umma_commit_pair(accfull);
+                if (ok && elect_one()) umma_commit_pair(accfull, both);
                 __syncwarp();
             }
-            if (elect_one()) umma_commit_pair(fin);       // always: arrives once every MMA issued above has completed
+            if (elect_one()) umma_commit_pair(fin, both); // always: arrives once every MMA issued above has completed
             __syncwarp();
         }
     } else if (warp < 11) {
@@ -435,7 +535,25 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(afull0 + 8 * s);
-                kb = kb + 1 == nk ? 0 : kb + 1;
+                kb = knext(kb);
+            }
+        }
+    } else if (C::kSplit) {
+        // ---- the pair's sums into shared memory, fp32 [token][128 rows], in
+        // the rings' space: every load and MMA of this CTA is done with it
+        const int qw = warp & 3, half = (warp - 11) >> 2;
+        const bool ok = mbar_wait(accfull, 0, kFaultGemmPair + kFaultEpilogueWait, abort) && !*abort;
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            const uint32_t at = sX + (uint32_t)(half * (BN / 2) * 128 + 32 * qw + lane) * 4;
+#pragma unroll 1
+            for (int c = 0; c < BN / 2; c += 32) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * qw) << 16) + half * (BN / 2) + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (uint32_t)(c + j) * 512), "r"(r[j]) : "memory");
             }
         }
     } else {
@@ -521,7 +639,12 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_arrive_wait();                                // neither CTA leaves while the other may still signal it
+    cluster_arrive_wait();                                // no CTA leaves while another may still signal it
+    if (C::kSplit) {
+        // every CTA finishes its rows of its pair's share of the tokens
+        if (*abort == 0) split_epilogue<BN, EPI>(a, sX, row_block0(first_tile), rank, pair, pairs);
+        cluster_arrive_wait();                            // the sums stay until every reader is done
+    }
     if (warp == 1) {
         // no MMA may still write tensor memory when it is released
         mbar_wait(fin, 0, kFaultGemmPair + kFaultDrainWait, nullptr);
@@ -532,50 +655,92 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 
 namespace {
 
-// Launch on as many clusters as can be resident (74 on 148 SMs), at most one per tile.
-template <int EPI>
-cudaError_t launch_pair(const CUtensorMap* tm, const PairArgs& a, cudaStream_t s) {
-    // kernel attributes and residency, once per device (double-checked under a lock)
-    static std::atomic<int> resident[64] = {};
+// Clusters of `pairs` CTA pairs that can be resident at once (74 pairs on 148
+// SMs), once per device; sets the kernel's attributes.
+template <int BN, int EPI>
+cudaError_t pair_clusters(int dev, int pairs, int* clusters) {
+    static std::atomic<int> resident[64][kMaxPairs + 1] = {};
     static std::mutex mu;
-    int dev = 0;
-    cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = resident[dev][pairs].load(std::memory_order_acquire);
+    if (n == 0) {
+        std::lock_guard<std::mutex> lock(mu);
+        auto k = gemm_pair_kernel<BN, EPI>;
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairCfg<BN>::kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 * pairs, 1, 1);
+        cfg.blockDim = dim3(kPairThreads, 1, 1);
+        cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 * pairs;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        resident[dev][pairs].store(n, std::memory_order_release);
+    }
+    *clusters = n;
+    return cudaSuccess;
+}
+
+template <int BN, int EPI>
+cudaError_t launch_pair(const CUtensorMap* tm, PairArgs& a, cudaStream_t s) {
+    int dev = 0, clusters = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    a.pairs = 1;
+    if (PairCfg<BN>::kSplit) {
+        // Pairs per tile: the fewest stages one after another, counting the
+        // rounds of clusters that do not fit at once; a round costs about six
+        // stages' time to start and end, a split two more for its exchange.
+        long best = 0;
+        for (int p = 1; p <= kMaxPairs && p <= a.nk; p *= 2) {
+            int n = 0;
+            e = pair_clusters<BN, EPI>(dev, p, &n);
+            if (e != cudaSuccess) return e;
+            const long cost = (long)((a.ntiles + n - 1) / n) * ((a.nk + p - 1) / p + 6 + (p > 1 ? 2 : 0));
+            if (best == 0 || cost < best) {
+                best = cost;
+                a.pairs = p;
+            }
+        }
+        clusters = a.ntiles;                               // one tile per cluster
+    } else {
+        e = pair_clusters<BN, EPI>(dev, 1, &clusters);
+        if (e != cudaSuccess) return e;
+        clusters = std::min(clusters, a.ntiles);
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2, 1, 1);
+    cfg.gridDim = dim3(2 * (unsigned)(a.pairs * clusters), 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 2 * a.pairs;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = resident[dev].load(std::memory_order_acquire);
-    if (clusters == 0) {
-        std::lock_guard<std::mutex> lock(mu);
-        clusters = resident[dev].load(std::memory_order_relaxed);
-        if (clusters == 0) {
-            cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)kPairSmem);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, gemm_pair_kernel<EPI>, &cfg);
-            if (e != cudaSuccess) return e;
-            if (clusters < 1) return cudaErrorLaunchOutOfResources;
-            resident[dev].store(clusters, std::memory_order_release);
-        }
-    }
-    cfg.gridDim = dim3(2 * (unsigned)std::min(clusters, a.ntiles), 1, 1);
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<EPI>, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<BN, EPI>, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
+}
+
+template <int BN>
+cudaError_t launch_pair_epi(const CUtensorMap* tm, PairArgs& a, bool gated, cudaStream_t s) {
+    a.ntiles = a.mt * ((a.T + BN - 1) / BN);
+    return gated ? launch_pair<BN, kEpiGated>(tm, a, s) : launch_pair<BN, kEpiAct>(tm, a, s);
 }
 
 }  // namespace
 
-// Tensor maps: X' fp16 [T][in], box 64 channels x 128 tokens, 128-byte
+// Tensor maps: X' fp16 [T][in], box 64 channels x BN / 2 tokens, 128-byte
 // swizzle; codes as uint32 [out/16][in/128 * 256], box 128 channels x 8 row
 // blocks; scales uint32 [out/16][G * 8], box the stage's groups x 8 row
 // blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y and
@@ -595,10 +760,13 @@ cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, co
     a.act = epi.act;
     a.has_res = epi.residual ? 1 : 0;
     a.bias = static_cast<const __half*>(bias);
+    a.residual = static_cast<const __half*>(epi.residual);
+    a.Y = static_cast<__half*>(Y);
+    const int BN = T <= 64 ? 64 : T <= 128 ? 128 : 256;
     const uint64_t G = (uint64_t)(in / group), Gp = G + (G & 1), nrb = (uint64_t)(out / 16);
     CUtensorMap tm[6];
     const bool ok =
-        encode_tma_2d(&tm[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xr, (uint64_t)in, (uint64_t)T, (uint64_t)in * 2, 64u, 128u,
+        encode_tma_2d(&tm[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xr, (uint64_t)in, (uint64_t)T, (uint64_t)in * 2, 64u, (uint32_t)BN / 2,
                       CU_TENSOR_MAP_SWIZZLE_128B) &&
         encode_tma_2d(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, (uint64_t)a.nk * 256, nrb, (uint64_t)a.nk * 1024, 256u, 8u,
                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
@@ -611,8 +779,9 @@ cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, co
                       (uint64_t)T, (uint64_t)a.width * 2, gated ? 16u : 32u, 32u, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) return cudaErrorInvalidValue;
     a.mt = (int)((nrb + 15) / 16);
-    a.ntiles = a.mt * (int)((T + 255) / 256);
-    const cudaError_t e = gated ? launch_pair<kEpiGated>(tm, a, s) : launch_pair<kEpiAct>(tm, a, s);
+    const cudaError_t e = BN == 64    ? launch_pair_epi<64>(tm, a, gated, s)
+                          : BN == 128 ? launch_pair_epi<128>(tm, a, gated, s)
+                                      : launch_pair_epi<256>(tm, a, gated, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

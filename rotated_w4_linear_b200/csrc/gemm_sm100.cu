@@ -59,8 +59,6 @@ struct GemmArgs {
     const __half* bias;         // [out] fp16 or null
     __half* Y;                  // fp16 [T][out], or
     float* Yf;                  // fp32 [T][out] unrounded sums (row-parallel partials) when not null
-    const __half* residual;     // kEpiAct: fp16 [T][out] or null (may be Y)
-    int act;                    // kEpiAct, kEpiGated
 };
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -74,48 +72,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t ra
     return v;
 }
 
-// Sixteen tokens of one accumulator row per thread -> activation, residual,
-// fp16, store. The residual's loads are issued before the activation.
-struct ActColumns {
-    const GemmArgs& a;
-    const uint32_t* r;
-    float b;
-    int t0, row;
-    template <int ACT>
-    __device__ __forceinline__ void run() const {
-        float res[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            res[j] = a.residual && t0 + j < a.T ? __half2float(a.residual[(size_t)(t0 + j) * a.out + row]) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (t0 + j < a.T)
-                a.Y[(size_t)(t0 + j) * a.out + row] = __float2half_rn(act_fn<ACT>(__uint_as_float(r[j]) + b) + res[j]);
-    }
-};
-
-// Gate rows (lanes with bit 3 clear) and up rows (8 lanes on) trade columns:
-// of tokens t, t + 1 the gate lane finishes t and the up lane t + 1. The whole
-// warp calls it; col < 0 stores nothing.
-struct GatedColumns {
-    const GemmArgs& a;
-    const uint32_t* r;
-    float b;                    // this row's own bias
-    int t0, col;
-    bool up;
-    template <int ACT>
-    __device__ __forceinline__ void run() const {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float v0 = __uint_as_float(r[j]) + b, v1 = __uint_as_float(r[j + 1]) + b;
-            const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-            const float h = act_fn<ACT>(up ? other : v0) * (up ? v1 : other);
-            const int t = t0 + j + (up ? 1 : 0);
-            if (col >= 0 && t < a.T) a.Y[(size_t)t * (a.out >> 1) + col] = __float2half_rn(h);
-        }
-    }
-};
-
 }  // namespace
 
 // BN: tokens per tile (MMA N); STAGES: pipeline depth; DQG: dequant warp
@@ -123,7 +79,7 @@ struct GatedColumns {
 // NACC: accumulators the MMAs rotate over. Consecutive MMAs into one
 // accumulator wait for each other's full latency, which dominates at small
 // N; independent accumulators let them overlap (summed in the epilogue).
-template <int BN, int STAGES, int DQG, int NACC, int EPI>
+template <int BN, int STAGES, int DQG, int NACC>
 __global__ void __launch_bounds__(64 + 128 * DQG, 1)
 gemm_w4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_z, const GemmArgs a) {
@@ -283,15 +239,7 @@ gemm_w4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
                 }
-                if (EPI == kEpiGated) {
-                    const bool up = lane & 8;
-                    const int col = (row >> 4) * 8 + (lane & 7);
-                    const bool in = row < a.out;
-                    const float b = a.bias && in ? __half2float(a.bias[col + (up ? a.out >> 1 : 0)]) : 0.f;
-                    with_act(a.act, GatedColumns{a, r, b, n0 + c0, in ? col : -1, up});
-                } else if (EPI == kEpiAct) {
-                    if (row < a.out) with_act(a.act, ActColumns{a, r, a.bias ? __half2float(a.bias[row]) : 0.f, n0 + c0, row});
-                } else if (a.nsplit > 1) {                // BN == 16: partial tile red[token][row]
+                if (a.nsplit > 1) {                       // BN == 16: partial tile red[token][row]
 #pragma unroll
                     for (int j = 0; j < 16; ++j) red[j * kRedStride + rloc] = __uint_as_float(r[j]);
                 } else if (row < a.out) {
@@ -381,7 +329,7 @@ bool encode_tma_2d(CUtensorMap* tm, CUtensorMapDataType type, const void* base, 
 
 namespace {
 
-template <int BN, int STAGES, int DQG, int NACC, int EPI>
+template <int BN, int STAGES, int DQG, int NACC>
 cudaError_t launch_cfg(const CUtensorMap* tm, const GemmArgs& a, int mt, int nt, cudaStream_t s) {
     constexpr size_t smem = STAGES * (BN * 128 + kWStage + kSStage + kZStage) + (3 * STAGES + 2) * 8 +
                             16 * (128 + 4) * 4 + 1024;
@@ -394,10 +342,10 @@ cudaError_t launch_cfg(const CUtensorMap* tm, const GemmArgs& a, int mt, int nt,
     if (!configured[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(mu);
         if (!configured[dev].load(std::memory_order_relaxed)) {
-            cudaError_t e = cudaFuncSetAttribute(gemm_w4_kernel<BN, STAGES, DQG, NACC, EPI>,
+            cudaError_t e = cudaFuncSetAttribute(gemm_w4_kernel<BN, STAGES, DQG, NACC>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(gemm_w4_kernel<BN, STAGES, DQG, NACC, EPI>,
+                e = cudaFuncSetAttribute(gemm_w4_kernel<BN, STAGES, DQG, NACC>,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             configured[dev].store(true, std::memory_order_release);
@@ -417,7 +365,7 @@ cudaError_t launch_cfg(const CUtensorMap* tm, const GemmArgs& a, int mt, int nt,
     attr[1].val.clusterDim.z = a.nsplit;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_w4_kernel<BN, STAGES, DQG, NACC, EPI>, tm[0], tm[1], tm[2], tm[3], a);
+    return cudaLaunchKernelEx(&cfg, gemm_w4_kernel<BN, STAGES, DQG, NACC>, tm[0], tm[1], tm[2], tm[3], a);
 }
 
 // tm[0]: X' [T][in] fp16, box 64 channels x BN tokens, 128-byte swizzle, zero fill past T
@@ -468,24 +416,17 @@ cudaError_t launch_gemm(const void* Xr, const void* qw, const void* scp, const v
                         const Epilogue& epi) {
     if (T <= 0) return cudaSuccess;
     if (group != 64 && group != 128) return cudaErrorInvalidValue;
-    if (epi.kind != kEpiPlain && T > 128) return launch_gemm_pair(Xr, qw, scp, zp, bias, Y, T, in, out, group, s, epi);
+    if (epi.kind != kEpiPlain) return launch_gemm_pair(Xr, qw, scp, zp, bias, Y, T, in, out, group, s, epi);
     const int BN = T <= 64 ? 64 : T <= 128 ? 128 : 256;
     GemmArgs a = make_args(T, in, out, group, scp, zp, bias, Y, y_fp32);
-    a.residual = static_cast<const __half*>(epi.residual);
-    a.act = epi.act;
     CUtensorMap tm[4];
     if (!encode_maps(Xr, qw, scp, zp, T, BN, a, tm)) return cudaErrorInvalidValue;
     const int mt = (a.nrb + 7) / 8;
     const int nt = (int)((T + BN - 1) / BN);
     cudaError_t e;
-    if (epi.kind == kEpiAct)
-        e = BN == 64 ? launch_cfg<64, 4, 1, 1, kEpiAct>(tm, a, mt, nt, s) : launch_cfg<128, 4, 1, 1, kEpiAct>(tm, a, mt, nt, s);
-    else if (epi.kind == kEpiGated)
-        e = BN == 64 ? launch_cfg<64, 4, 1, 1, kEpiGated>(tm, a, mt, nt, s)
-                     : launch_cfg<128, 4, 1, 1, kEpiGated>(tm, a, mt, nt, s);
-    else if (BN == 64) e = launch_cfg<64, 4, 1, 1, kEpiPlain>(tm, a, mt, nt, s);
-    else if (BN == 128) e = launch_cfg<128, 4, 1, 1, kEpiPlain>(tm, a, mt, nt, s);
-    else e = launch_cfg<256, 4, 1, 1, kEpiPlain>(tm, a, mt, nt, s);
+    if (BN == 64) e = launch_cfg<64, 4, 1, 1>(tm, a, mt, nt, s);
+    else if (BN == 128) e = launch_cfg<128, 4, 1, 1>(tm, a, mt, nt, s);
+    else e = launch_cfg<256, 4, 1, 1>(tm, a, mt, nt, s);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -80,7 +80,7 @@ cudaError_t launch_gemv_noalloc(const RotDev* rot, const void* X, const void* qw
 cudaError_t launch_gemm(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
                         int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, bool y_fp32 = false,
                         const Epilogue& epi = Epilogue());
-// Prefill above 128 tokens on CTA pairs (gemm_pair_sm100.cu): the same product with 256-row x 256-token tiles.
+// Above 16 tokens on CTA pairs (gemm_pair_sm100.cu), with the epilogues kEpiAct and kEpiGated.
 cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
                              int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, const Epilogue& epi);
 
