@@ -13,11 +13,11 @@
 //     cores): one tile per cluster, whose 1, 2 or 4 pairs split the channels,
 //     since the row tiles alone would leave most SMs idle; the pairs' sums
 //     meet through distributed shared memory in a fixed order.
-// Per CTA, nineteen warps:
-//   warp 0      TMA producer: per stage of 128 channels the CTA's half of the
-//               tokens of X' (two 64-channel boxes, 128-byte swizzle) and, two
-//               stages ahead of it, the int4 codes of its 8 row blocks with
-//               their scales and zeros;
+// Per CTA, twenty warps:
+//   warps 0, 19 TMA producers: per stage of 128 channels the CTA's half of the
+//               tokens of X' (two 64-channel boxes, 128-byte swizzle), and the
+//               int4 codes of its 8 row blocks with their scales and zeros,
+//               whose ring is two stages deeper;
 //   warps 3-10  dequantise (w_hat = fp16((q - z) s), as the other kernels do)
 //               into a ring of tensor-memory stages: a warp takes one quarter
 //               of the rows and one half of the stage's channels;
@@ -60,7 +60,7 @@ namespace paro {
 
 namespace {
 
-constexpr int kPairThreads = 608;
+constexpr int kPairThreads = 640;
 constexpr uint32_t kWCodes = 8 * 1024;                  // 8 row blocks x 128 channels of codes
 constexpr uint32_t kWScales = 8 * 64;                   // 8 row blocks x up to 2 groups x 8 words
 constexpr uint32_t kWStage = kWCodes + kWScales + 128;  // zeros: 8 row blocks x 2 groups x 8 bytes
@@ -105,6 +105,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive_wait() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Without memory ordering (the readers' values are in use already): a release
+// would also wait for this CTA's stores of Y.
+__device__ __forceinline__ void cluster_arrive_wait_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -372,70 +377,55 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     auto kstart = [&](int tile) { return k0 + (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
     auto knext = [&](int kb) { return kb + 1 == k0 + nk ? k0 : kb + 1; };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // ---- TMA producer: the weights of a stage go out two stages
-            // before its X', so they never wait behind an X' slot
-            constexpr int kAhead = kWStages - kXStages;
-            RingPos<kXStages> px;
-            RingPos<kWStages> pw;
-            uint32_t xissued[kXStages], wissued[kWStages];    // loads issued so far per slot (for the drain)
+    if (warp == 0 || warp == 19) {
+        // ---- TMA producers: X' (warp 0), weights (warp 19). As with the MMAs,
+        // the whole warp walks the stages and one elected lane issues.
+        const bool xs = warp == 0;
+        RingPos<kXStages> px;
+        RingPos<kWStages> pw;
+        uint32_t issued[kWStages];                        // loads issued so far per slot (for the drain)
 #pragma unroll
-            for (int s = 0; s < kXStages; ++s) xissued[s] = 0;
-#pragma unroll
-            for (int s = 0; s < kWStages; ++s) wissued[s] = 0;
-            int wtile = first_tile, wi = 0, wkb = wtile < a.ntiles ? kstart(wtile) : 0;
-            auto issue_w = [&]() {                        // the next stage's weights, if there is one
-                if (wtile >= a.ntiles) return true;
-                if (pw.use > 0 && !mbar_wait(wfree0 + 8 * pw.slot, (pw.use - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort))
-                    return false;
-                const int rb0 = row_block0(wtile);
-                const uint32_t bar = wfull0 + 8 * pw.slot, dst = sW + pw.slot * kWStage;
-                mbar_arrive_expect_tx(bar, kWCodes + 8 * 32 * a.gs + 128);
-                tma_load_2d(dst, &tm_w, wkb * 256, rb0, bar);
-                tma_load_2d(dst + kWCodes, &tm_s, wkb * 8 * a.gs, rb0, bar);
-                tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? wkb : wkb >> 1) * 16, rb0, bar);
+        for (int s = 0; s < kWStages; ++s) issued[s] = 0;
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
+            const int rb0 = row_block0(tile), n0 = token0(tile) + BN / 2 * (int)rank;
+            int kb = kstart(tile);
+            for (int i = 0; i < nk; ++i) {
+                const int slot = xs ? px.slot : pw.slot;
+                const uint32_t use = xs ? px.use : pw.use;
+                ok = use == 0 || mbar_wait((xs ? free0 : wfree0) + 8 * slot, (use - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort);
+                ok = __all_sync(0xffffffffu, ok && !*abort);
+                if (!ok) break;
+                if (xs) {
+                    const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, kXStage);
+                        tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
+                        tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
+                    }
+                    px.next();
+                } else {
+                    const uint32_t bar = wfull0 + 8 * slot, dst = sW + slot * kWStage;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, kWCodes + 8 * 32 * a.gs + 128);
+                        tma_load_2d(dst, &tm_w, kb * 256, rb0, bar);
+                        tma_load_2d(dst + kWCodes, &tm_s, kb * 8 * a.gs, rb0, bar);
+                        tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? kb : kb >> 1) * 16, rb0, bar);
+                    }
+                    pw.next();
+                }
+                __syncwarp();
 #pragma unroll
                 for (int t = 0; t < kWStages; ++t)
-                    if (t == pw.slot) wissued[t] = pw.use + 1;
-                pw.next();
-                wkb = knext(wkb);
-                if (++wi == nk) {
-                    wi = 0;
-                    wtile += nclusters;
-                    if (wtile < a.ntiles) wkb = kstart(wtile);
-                }
-                return true;
-            };
-            bool ok = true;
-            for (int i = 0; ok && i < kAhead; ++i) ok = issue_w();
-            for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
-                const int n0 = token0(tile) + BN / 2 * (int)rank;
-                int kb = kstart(tile);
-                for (int i = 0; i < nk; ++i) {
-                    ok = issue_w() && (px.use == 0 || mbar_wait(free0 + 8 * px.slot, (px.use - 1) & 1,
-                                                                kFaultGemmPair + kFaultTmaWait, abort)) && !*abort;
-                    if (!ok) break;
-                    const uint32_t bar = xfull0 + 8 * px.slot, dst = sX + px.slot * kXStage;
-                    mbar_arrive_expect_tx(bar, kXStage);
-                    tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
-                    tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
-#pragma unroll
-                    for (int t = 0; t < kXStages; ++t)
-                        if (t == px.slot) xissued[t] = px.use + 1;
-                    px.next();
-                    kb = knext(kb);
-                }
-            }
-            if (*abort) {   // drain: every issued load must land before the CTA exits
-#pragma unroll
-                for (int s = 0; s < kXStages; ++s)
-                    if (xissued[s] > 0) mbar_wait(xfull0 + 8 * s, (xissued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
-#pragma unroll
-                for (int s = 0; s < kWStages; ++s)
-                    if (wissued[s] > 0) mbar_wait(wfull0 + 8 * s, (wissued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
+                    if (t == slot) issued[t] = use + 1;
+                kb = knext(kb);
             }
         }
+        if (*abort)   // drain: every issued load must land before the CTA exits
+#pragma unroll
+            for (int s = 0; s < kWStages; ++s)
+                if (issued[s] > 0)
+                    mbar_wait((xs ? xfull0 : wfull0) + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
     } else if (warp == 2) {
         if (lane == 0) {
             // ---- gate: one report per stage to the leader's MMA thread, which
@@ -643,7 +633,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     if (C::kSplit) {
         // every CTA finishes its rows of its pair's share of the tokens
         if (*abort == 0) split_epilogue<BN, EPI>(a, sX, row_block0(first_tile), rank, pair, pairs);
-        cluster_arrive_wait();                            // the sums stay until every reader is done
+        cluster_arrive_wait_relaxed();                    // the sums stay until every reader is done
     }
     if (warp == 1) {
         // no MMA may still write tensor memory when it is released
