@@ -5,12 +5,12 @@
 // Two CTAs of a cluster share a tile: each keeps its own 128 rows of w_hat in
 // its tensor memory and holds half of the tokens in shared memory, and one
 // MMA (M = 256, N = BN, K = 16) reads both halves. Two forms:
-//   BN = 256 (above 128 tokens; bound by the tensor cores and their power):
+//   BN = 256 (many tiles; bound by the tensor cores and their power):
 //     persistent; a cluster of one pair walks the tiles cid, cid + clusters,
 //     ... (row tiles first, so that the clusters at work share their tokens)
 //     and its roles run ahead of each other across tiles;
-//   BN = 64, 128 (17 to 128 tokens; bound by the weights' way to the tensor
-//     cores): one tile per cluster, whose 1, 2 or 4 pairs split the channels,
+//   BN = 64, 128 (17 to 128 tokens, and more where the tiles of 256 would be
+//     few; bound by the weights' way to the tensor cores): one tile per cluster, whose one to four pairs split the channels,
 //     since the row tiles alone would leave most SMs idle; the pairs' sums
 //     meet through distributed shared memory in a fixed order.
 // Per CTA, twenty warps:
@@ -31,9 +31,10 @@
 //               into registers (after the second 64 the accumulator is free
 //               for the next tile), then through a 32-token buffer of its own
 //               in shared memory, where the residual has arrived by TMA, to a
-//               TMA store. BN < 256: the warps put the fp32 sums into shared
-//               memory (the rings' space), and after a cluster barrier all
-//               warps add the pairs' sums, apply the epilogue and store.
+//               TMA store. BN < 256: these warps dequantise every second
+//               stage; then all sixteen put the fp32 sums into shared memory
+//               (the rings' space), and after a cluster barrier all warps add
+//               the pairs' sums, apply the epilogue and store.
 // All waits are bounded (sm100.cuh); a wait that runs out raises the CTA's
 // abort flag, every role stops, what was issued is drained, and the cluster's
 // CTAs meet at the last barrier.
@@ -43,8 +44,8 @@
 // with a cluster-scope release by each dequantisation warp it took 1766, with
 // the MMAs issued from a one-lane branch 1246.
 //
-// With BN = 256 a token's result does not depend on its place in the batch:
-// the order of the channels goes by the row tile alone.
+// A token's result does not depend on its place in the batch: the order of the
+// channels goes by the row tile and the split alone.
 #include <cuda.h>
 
 #include <algorithm>
@@ -229,14 +230,14 @@ struct PairGated {
 };
 
 // BN < 256: the pairs' sums of this CTA's rows, added in pair order, to the
-// output: tokens [BN pair / pairs, BN (pair + 1) / pairs), four rows (gated:
+// output: tokens [BN pair / pairs, BN (pair + 1) / pairs) of the tile, four rows (gated:
 // four gate and four up rows) of one token per thread and step. A CTA whose
 // rows or tokens lie outside takes no part.
 template <int BN, int EPI>
-__device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums, int rb0, uint32_t rank, int pair,
-                                               int pairs) {
+__device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums, int rb0, int n0, uint32_t rank,
+                                               int pair, int pairs) {
     constexpr int kFours = EPI == kEpiGated ? 16 : 32;     // fours per token
-    const int t0 = BN * pair / pairs, t1 = min(a.T, BN * (pair + 1) / pairs);
+    const int t0 = BN * pair / pairs, t1 = min(a.T - n0, BN * (pair + 1) / pairs);
     const int c0 = EPI == kEpiGated ? rb0 * 8 : rb0 * 16;
     for (int i = threadIdx.x; i < (t1 - t0) * kFours; i += kPairThreads) {
         const int t = t0 + i / kFours, k = i % kFours;
@@ -273,7 +274,7 @@ __device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums,
         };
         float4 y = sum(v, c);
         y = make_float4(act_any(y.x, a.act), act_any(y.y, a.act), act_any(y.z, a.act), act_any(y.w, a.act));
-        const size_t to = (size_t)t * a.width + c;
+        const size_t to = (size_t)(n0 + t) * a.width + c;
         if (EPI == kEpiGated) {
             const float4 w = sum(u, a.width + c);
             y = make_float4(y.x * w.x, y.y * w.y, y.z * w.z, y.w * w.w);
@@ -480,17 +481,23 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (elect_one()) umma_commit_pair(fin, both); // always: arrives once every MMA issued above has completed
             __syncwarp();
         }
-    } else if (warp < 11) {
-        // ---- dequantisation
+    } else if (C::kSplit || warp < 11) {
+        // ---- dequantisation (BN < 256: two groups of eight warps take turns)
         const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
-        const int half = (warp - 3) >> 2;                 // channels 64 half .. + 63 of a stage
+        const int half = ((warp - 3) >> 2) & 1;           // channels 64 half .. + 63 of a stage
+        // A slot's uses must all be one group's, for its waits by phase parity
+        constexpr int kGroups = C::kSplit ? 2 : 1;
+        static_assert(kXStages % kGroups == 0 && kWStages % kGroups == 0, "every slot belongs to one group");
+        const int group = C::kSplit ? (warp - 3) >> 3 : 0;
         const int g = lane >> 2;
         RingPos<kXStages> p;
         RingPos<kWStages> pw;
         bool ok = true;
+        if (group) p.next(), pw.next();
         for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
             int kb = kstart(tile);
-            for (int i = 0; i < nk; ++i, p.next(), pw.next()) {
+            if (group) kb = knext(kb);
+            for (int i = group; i < nk; i += kGroups) {
                 const int s = p.slot;
                 // the tensor-memory stores below are warp-collective: the whole
                 // warp goes on only if every lane saw the stage arrive
@@ -525,25 +532,32 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(afull0 + 8 * s);
-                kb = knext(kb);
+#pragma unroll
+                for (int e = 0; e < kGroups; ++e) {
+                    kb = knext(kb);
+                    p.next();
+                    pw.next();
+                }
             }
         }
-    } else if (C::kSplit) {
-        // ---- the pair's sums into shared memory, fp32 [token][128 rows], in
-        // the rings' space: every load and MMA of this CTA is done with it
-        const int qw = warp & 3, half = (warp - 11) >> 2;
-        const bool ok = mbar_wait(accfull, 0, kFaultGemmPair + kFaultEpilogueWait, abort) && !*abort;
-        if (__all_sync(0xffffffffu, ok)) {
-            tc_fence_after();
-            const uint32_t at = sX + (uint32_t)(half * (BN / 2) * 128 + 32 * qw + lane) * 4;
-#pragma unroll 1
-            for (int c = 0; c < BN / 2; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * qw) << 16) + half * (BN / 2) + c, r);
-                tmem_wait_ld();
+        if (C::kSplit) {
+            // ---- the pair's sums into shared memory, fp32 [token][128 rows],
+            // in the rings' space: every load and MMA of this CTA is done with
+            // it. A warp takes its quarter of the rows of a quarter of the tokens.
+            const int quarter = (warp - 3) >> 2;
+            ok = mbar_wait(accfull, 0, kFaultGemmPair + kFaultEpilogueWait, abort) && !*abort;
+            if (__all_sync(0xffffffffu, ok)) {
+                tc_fence_after();
+                const uint32_t at = sX + (uint32_t)(quarter * (BN / 4) * 128 + 32 * qw + lane) * 4;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (uint32_t)(c + j) * 512), "r"(r[j]) : "memory");
+                for (int c = 0; c < BN / 4; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(tbase + ((uint32_t)(32 * qw) << 16) + quarter * (BN / 4) + c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (uint32_t)(c + j) * 512), "r"(r[j]) : "memory");
+                }
             }
         }
     } else {
@@ -632,7 +646,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     cluster_arrive_wait();                                // no CTA leaves while another may still signal it
     if (C::kSplit) {
         // every CTA finishes its rows of its pair's share of the tokens
-        if (*abort == 0) split_epilogue<BN, EPI>(a, sX, row_block0(first_tile), rank, pair, pairs);
+        if (*abort == 0) split_epilogue<BN, EPI>(a, sX, row_block0(first_tile), token0(first_tile), rank, pair, pairs);
         cluster_arrive_wait_relaxed();                    // the sums stay until every reader is done
     }
     if (warp == 1) {
@@ -678,30 +692,43 @@ cudaError_t pair_clusters(int dev, int pairs, int* clusters) {
     return cudaSuccess;
 }
 
+// What a product takes in each form, in SM cycles: rounds of tiles that do not
+// fit at once, times a tile's stages and its start and end. The figures are
+// measured (4096 -> 28672 and 14336 -> 4096, 17 to 512 tokens): a stage of the
+// 256-token form 1250 and a tile's change-over 4000; a stage of the split form
+// 800, its start, exchange and end 11000, 1500 more with several pairs. Taking
+// the cheaper one, 4096 -> 4096 at 256 tokens runs in the split form (32 tiles
+// of 128 tokens, two pairs each) and 4096 -> 28672 at 256 in the other.
+struct PairPlan {
+    long cost = 0;
+    int pairs = 1;
+};
 template <int BN, int EPI>
-cudaError_t launch_pair(const CUtensorMap* tm, PairArgs& a, cudaStream_t s) {
-    int dev = 0, clusters = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    a.pairs = 1;
-    if (PairCfg<BN>::kSplit) {
-        // Pairs per tile: the fewest stages one after another, counting the
-        // rounds of clusters that do not fit at once; a round costs about six
-        // stages' time to start and end, a split two more for its exchange.
-        long best = 0;
-        for (int p = 1; p <= kMaxPairs && p <= a.nk; p *= 2) {
-            int n = 0;
-            e = pair_clusters<BN, EPI>(dev, p, &n);
-            if (e != cudaSuccess) return e;
-            const long cost = (long)((a.ntiles + n - 1) / n) * ((a.nk + p - 1) / p + 6 + (p > 1 ? 2 : 0));
-            if (best == 0 || cost < best) {
-                best = cost;
-                a.pairs = p;
-            }
+cudaError_t plan_pair(int dev, const PairArgs& a, PairPlan* plan) {
+    const int tiles = a.mt * ((a.T + BN - 1) / BN);
+    *plan = PairPlan();
+    for (int p = 1; p <= (PairCfg<BN>::kSplit ? std::min(kMaxPairs, a.nk) : 1); ++p) {
+        int n = 0;
+        const cudaError_t e = pair_clusters<BN, EPI>(dev, p, &n);
+        if (e != cudaSuccess) return e;
+        const long rounds = (tiles + n - 1) / n, stages = (a.nk + p - 1) / p;
+        const long cost = PairCfg<BN>::kSplit ? rounds * (stages * 800 + 11000 + (p > 1 ? 1500 : 0))
+                                              : rounds * (stages * 1250 + 4000) + 6000;
+        if (plan->cost == 0 || cost < plan->cost) {
+            plan->cost = cost;
+            plan->pairs = p;
         }
-        clusters = a.ntiles;                               // one tile per cluster
-    } else {
-        e = pair_clusters<BN, EPI>(dev, 1, &clusters);
+    }
+    return cudaSuccess;
+}
+
+template <int BN, int EPI>
+cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPlan& plan, cudaStream_t s) {
+    a.ntiles = a.mt * ((a.T + BN - 1) / BN);
+    a.pairs = plan.pairs;
+    int clusters = a.ntiles;                               // split form: one tile per cluster
+    if (!PairCfg<BN>::kSplit) {
+        const cudaError_t e = pair_clusters<BN, EPI>(dev, 1, &clusters);
         if (e != cudaSuccess) return e;
         clusters = std::min(clusters, a.ntiles);
     }
@@ -719,23 +746,61 @@ cudaError_t launch_pair(const CUtensorMap* tm, PairArgs& a, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<BN, EPI>, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, gemm_pair_kernel<BN, EPI>, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int BN>
-cudaError_t launch_pair_epi(const CUtensorMap* tm, PairArgs& a, bool gated, cudaStream_t s) {
-    a.ntiles = a.mt * ((a.T + BN - 1) / BN);
-    return gated ? launch_pair<BN, kEpiGated>(tm, a, s) : launch_pair<BN, kEpiAct>(tm, a, s);
+// The operands' tensor maps: X' fp16 [T][in], box 64 channels x BN / 2 tokens,
+// 128-byte swizzle; codes as uint32 [out/16][in/128 * 256], box 128 channels x
+// 8 row blocks; scales uint32 [out/16][G * 8], box the stage's groups x 8 row
+// blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y and
+// the residual fp16 [T][width], box 32 (gated: 16) columns x 32 tokens (used by
+// the 256-token form). Rows past T or out are read as zeros and not written.
+template <int BN, int EPI>
+cudaError_t encode_and_launch(int dev, const void* Xr, const void* qw, const void* scp, const void* zp, int64_t in,
+                              int group, const PairArgs& a, const PairPlan& plan, cudaStream_t s) {
+    const uint64_t G = (uint64_t)(in / group), Gp = G + (G & 1), nrb = (uint64_t)(a.out / 16);
+    const uint32_t cols = EPI == kEpiGated ? 16u : 32u;
+    CUtensorMap tm[6];
+    const bool ok =
+        encode_tma_2d(&tm[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xr, (uint64_t)in, (uint64_t)a.T, (uint64_t)in * 2, 64u,
+                      (uint32_t)BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+        encode_tma_2d(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, (uint64_t)a.nk * 256, nrb, (uint64_t)a.nk * 1024, 256u, 8u,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
+        encode_tma_2d(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, scp, G * 8, nrb, G * 32, 8u * (uint32_t)a.gs, 8u,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
+        encode_tma_2d(&tm[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, zp, Gp * 8, nrb, Gp * 8, 16u, 8u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+        encode_tma_2d(&tm[4], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.Y, (uint64_t)a.width, (uint64_t)a.T, (uint64_t)a.width * 2,
+                      cols, 32u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+        encode_tma_2d(&tm[5], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.residual ? a.residual : a.Y, (uint64_t)a.width,
+                      (uint64_t)a.T, (uint64_t)a.width * 2, cols, 32u, CU_TENSOR_MAP_SWIZZLE_NONE);
+    return ok ? launch_pair<BN, EPI>(dev, tm, a, plan, s) : cudaErrorInvalidValue;
+}
+
+// 17 to 64 tokens: tiles of 64; to 128: tiles of 128; above: the cheaper of
+// the split form with tiles of 128 and the persistent one with tiles of 256.
+template <int EPI>
+cudaError_t plan_and_launch(const void* Xr, const void* qw, const void* scp, const void* zp, int64_t in, int group,
+                            const PairArgs& a, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    PairPlan split, whole;
+    if (a.T <= 64) {
+        e = plan_pair<64, EPI>(dev, a, &split);
+        return e != cudaSuccess ? e : encode_and_launch<64, EPI>(dev, Xr, qw, scp, zp, in, group, a, split, s);
+    }
+    e = plan_pair<128, EPI>(dev, a, &split);
+    if (e == cudaSuccess && a.T > 128) e = plan_pair<256, EPI>(dev, a, &whole);
+    if (e != cudaSuccess) return e;
+    return a.T <= 128 || split.cost < whole.cost
+               ? encode_and_launch<128, EPI>(dev, Xr, qw, scp, zp, in, group, a, split, s)
+               : encode_and_launch<256, EPI>(dev, Xr, qw, scp, zp, in, group, a, whole, s);
 }
 
 }  // namespace
 
-// Tensor maps: X' fp16 [T][in], box 64 channels x BN / 2 tokens, 128-byte
-// swizzle; codes as uint32 [out/16][in/128 * 256], box 128 channels x 8 row
-// blocks; scales uint32 [out/16][G * 8], box the stage's groups x 8 row
-// blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y and
-// the residual fp16 [T][width], box 32 (gated: 16) columns x 32 tokens. Rows past T or out are read as zeros and not
-// written.
 cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, const void* zp, const void* bias, void* Y,
                              int64_t T, int64_t in, int64_t out, int group, cudaStream_t s, const Epilogue& epi) {
     if (T <= 0) return cudaSuccess;
@@ -745,6 +810,7 @@ cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, co
     a.T = (int)T;
     a.out = (int)out;
     a.nk = (int)(in / 128);
+    a.mt = (int)((out / 16 + 15) / 16);
     a.width = (int)(gated ? out / 2 : out);
     a.gs = group == 64 ? 2 : 1;
     a.act = epi.act;
@@ -752,27 +818,8 @@ cudaError_t launch_gemm_pair(const void* Xr, const void* qw, const void* scp, co
     a.bias = static_cast<const __half*>(bias);
     a.residual = static_cast<const __half*>(epi.residual);
     a.Y = static_cast<__half*>(Y);
-    const int BN = T <= 64 ? 64 : T <= 128 ? 128 : 256;
-    const uint64_t G = (uint64_t)(in / group), Gp = G + (G & 1), nrb = (uint64_t)(out / 16);
-    CUtensorMap tm[6];
-    const bool ok =
-        encode_tma_2d(&tm[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xr, (uint64_t)in, (uint64_t)T, (uint64_t)in * 2, 64u, (uint32_t)BN / 2,
-                      CU_TENSOR_MAP_SWIZZLE_128B) &&
-        encode_tma_2d(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, (uint64_t)a.nk * 256, nrb, (uint64_t)a.nk * 1024, 256u, 8u,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
-        encode_tma_2d(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, scp, G * 8, nrb, G * 32, 8u * (uint32_t)a.gs, 8u,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
-        encode_tma_2d(&tm[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, zp, Gp * 8, nrb, Gp * 8, 16u, 8u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-        encode_tma_2d(&tm[4], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Y, (uint64_t)a.width, (uint64_t)T, (uint64_t)a.width * 2,
-                      gated ? 16u : 32u, 32u, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-        encode_tma_2d(&tm[5], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, epi.residual ? epi.residual : Y, (uint64_t)a.width,
-                      (uint64_t)T, (uint64_t)a.width * 2, gated ? 16u : 32u, 32u, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (!ok) return cudaErrorInvalidValue;
-    a.mt = (int)((nrb + 15) / 16);
-    const cudaError_t e = BN == 64    ? launch_pair_epi<64>(tm, a, gated, s)
-                          : BN == 128 ? launch_pair_epi<128>(tm, a, gated, s)
-                                      : launch_pair_epi<256>(tm, a, gated, s);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return gated ? plan_and_launch<kEpiGated>(Xr, qw, scp, zp, in, group, a, s)
+                 : plan_and_launch<kEpiAct>(Xr, qw, scp, zp, in, group, a, s);
 }
 
 cudaError_t read_fault_gemm_pair(unsigned int* code, bool clear) { return read_fault_word(code, clear); }

@@ -94,6 +94,8 @@ def test_group_sizes(B, T, group, rotated):
 @pytest.mark.parametrize("T,n_in,n_out", [
     (1, 14336, 4096), (16, 4096, 4096), (5, 17408, 5120),     # decode: split k, deep chunks
     (3, 256, 17408), (16, 2560, 19456),                       # wide: one k chunk, several row blocks per warp
+    (40, 14336, 4096), (100, 4096, 6144), (77, 2560, 9744),   # prefill, split channels
+    (200, 4096, 28672), (256, 4096, 4096), (500, 9728, 2560),
     (2048, 4096, 4096), (1000, 14336, 2576), (300, 5120, 34832),
 ])
 def test_layer_sizes(B, T, n_in, n_out):
@@ -150,11 +152,12 @@ def test_the_same_bits_in_every_call(B, T, n_in, n_out):
         assert torch.equal(p, B.paro_linear(L.rot, L.x, *L.packed, n_out))
 
 
-def test_a_token_does_not_depend_on_its_place_in_a_prefill_batch(B):
-    L = Layer(B, 700, 1024, 528, gated=True, seed=2)
-    h = B.paro_linear_gated(L.rot, L.x, *L.packed, 264, bias=L.bias)
-    for lo, hi in ((100, 700), (571, 700), (0, 257)):
-        assert torch.equal(h[lo:hi], B.paro_linear_gated(L.rot, L.x[lo:hi], *L.packed, 264, bias=L.bias))
+@pytest.mark.parametrize("T,inter", [(40, 264), (100, 264), (300, 264), (700, 9728)])
+def test_a_token_does_not_depend_on_its_place_in_the_batch(B, T, inter):
+    L = Layer(B, T, 1024, 2 * inter, gated=True, seed=2)
+    h = B.paro_linear_gated(L.rot, L.x, *L.packed, inter, bias=L.bias)
+    order = torch.randperm(T, device="cuda", generator=torch.Generator(device="cuda").manual_seed(T))
+    assert torch.equal(h[order], B.paro_linear_gated(L.rot, L.x[order].contiguous(), *L.packed, inter, bias=L.bias))
 
 
 @pytest.mark.parametrize("T", [4, 16, 70, 300])
