@@ -207,6 +207,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     unsigned char* ring = reinterpret_cast<unsigned char*>(red + NT * 8 * SR);
     const uint32_t ring_w = smem_u32(ring) + (uint32_t)(warp * kStages * kItemBytes);
 
+    // Warps whose runs begin inside row block rb: join[rb].x <= w < join[rb].y
+    // (their sums are added to the block's at the end).
+    __shared__ uint2 join[64];
+    if ((int)threadIdx.x < nrbt) {
+        const int f0 = (int)threadIdx.x * ncg;
+        uint32_t w = 1;
+        while (w < kWarps && (F * (int)w) / kWarps <= f0) ++w;
+        join[threadIdx.x].x = w;
+        while (w < kWarps && (F * (int)w) / kWarps < f0 + ncg) ++w;
+        join[threadIdx.x].y = w;
+    }
+
     // producer cursor: position, row block and group of the next item to
     // copy and the lane's source pointers, advanced incrementally
     int p_f = f_lo, p_rb = rb_begin + rbl_lo, p_g = g_lo;
@@ -405,11 +417,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     const int row0 = rb_begin * 16;
     auto tile_sum4 = [&](int t, int r) {
         float4 v = *reinterpret_cast<const float4*>(red + t * SR + r);
-        const int rb = r >> 4, f0 = rb * ncg;
-        for (int w = max(1, kWarps * rb / max(nrbt, 1)); w < kWarps; ++w) {
-            const int lo = (int)(((int64_t)F * w) / kWarps);
-            if (lo >= f0 + ncg) break;
-            if (lo <= f0 || lo == (int)(((int64_t)F * (w + 1)) / kWarps)) continue;   // owns the block, or has no run
+        const uint2 j = join[r >> 4];
+        for (uint32_t w = j.x; w < j.y; ++w) {
+            if (F < kWarps && (F * (int)w) / kWarps == (F * (int)(w + 1)) / kWarps) continue;   // a warp without a run
             const float4 u = *reinterpret_cast<const float4*>(
                 reinterpret_cast<const float*>(ring + (size_t)w * kStages * kItemBytes) + t * kJoinStride + (r & 15));
             v.x += u.x;
@@ -477,7 +487,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) gemv_kernel(const GemvArgs a) 
     // the joining warps' sums go into the tile before the other CTAs read it
     for (int i = threadIdx.x; i < a.T * nrbt * 4; i += kWarps * 32) {
         const int t = i / (nrbt * 4), r = 4 * (i - t * nrbt * 4);
-        *reinterpret_cast<float4*>(red + t * SR + r) = tile_sum4(t, r);
+        const uint2 j = join[r >> 4];
+        if (j.x < j.y) *reinterpret_cast<float4*>(red + t * SR + r) = tile_sum4(t, r);
     }
     cluster_sync();
     const int rlo = chunk * a.share;
