@@ -65,6 +65,28 @@ def gather_columns(Y, bounds, process_group=None):
     return torch.cat([p[:, :hi - lo] for p, (lo, hi) in zip(parts, bounds)], dim=1)
 
 
+def gather_tokens(Q, S, counts, process_group=None):
+    """Every rank's tokens in rank order, from shards in 8 bits: Q
+    [counts[rank]][features] (float8_e4m3fn codes) and S (fp32 scales) of
+    paro_rmsnorm_q8, counts the number of tokens on each rank. Half the bytes
+    of an fp16 exchange. The shards are padded to the largest (all_gather takes
+    equal sizes)."""
+    import torch
+    import torch.distributed as dist
+    most = max(counts)
+
+    def gathered(t):
+        pad = torch.zeros((most, t.shape[1]), dtype=t.dtype, device=t.device)
+        pad[:t.shape[0]] = t
+        parts = [torch.empty_like(pad) for _ in counts]
+        dist.all_gather(parts, pad, group=process_group)
+        return torch.cat([p[:n] for p, n in zip(parts, counts)])
+
+    if Q.shape[0] != S.shape[0] or Q.shape[0] != counts[dist.get_rank(process_group)]:
+        raise ValueError("Q and S must hold this rank's tokens, counts[rank] of them")
+    return gathered(Q.view(torch.uint8)).view(Q.dtype), gathered(S)
+
+
 class ColumnParallelLinear:
     """This rank's part of a column-parallel layer. The parameters are given
     whole (host arrays: the rotation's pairs, theta, alpha and the logical q,
@@ -105,6 +127,15 @@ class ColumnParallelLinear:
         if not (dist.is_available() and dist.is_initialized()):
             return Y
         return gather_columns(Y, self.bounds, process_group)
+
+    def forward_q8(self, Q, S, counts=None, scale_group: int = 128, process_group=None, gather: bool = False):
+        """forward() on a hidden state in 8 bits: the codes and scales of
+        paro_rmsnorm_q8 for this rank's tokens, gathered from all ranks
+        (counts[r] tokens on rank r) and restored to fp16 here. Without counts,
+        Q and S already hold every token."""
+        if counts is not None:
+            Q, S = gather_tokens(Q, S, counts, process_group)
+        return self.forward(B.paro_q8_expand(Q, S, scale_group), process_group, gather)
 
     def close(self):
         if self.rot is not None:

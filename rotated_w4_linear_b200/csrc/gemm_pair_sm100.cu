@@ -5,8 +5,8 @@
 // Two CTAs of a cluster share a tile: each keeps its own 128 rows of w_hat in
 // its tensor memory and holds half of the tokens in shared memory, and one
 // MMA (M = 256, N = BN, K = 16) reads both halves. Two forms:
-//   BN = 256 (many tiles; bound by the tensor cores and their power):
-//     persistent; a cluster of one pair walks the tiles cid, cid + clusters,
+//   BN = 256 (many tiles, of up to 256 tokens; bound by the tensor cores and
+//     their power): persistent; a cluster of one pair walks the tiles cid, cid + clusters,
 //     ... (row tiles first, so that the clusters at work share their tokens)
 //     and its roles run ahead of each other across tiles;
 //   BN = 64, 128 (17 to 128 tokens, and more where the tiles of 256 would be
@@ -90,6 +90,7 @@ constexpr int kMaxPairs = 4;                            // pairs that may split 
 struct PairArgs {
     int T, out, nk;             // nk: 128-channel stages
     int mt, ntiles;             // 256-row tiles; tiles in all
+    int bn;                     // tokens per tile: BN, or for BN = 256 a multiple of 32 up to it
     int pairs;                  // pairs per cluster (BN < 256: they split the channels)
     int width;                  // columns of Y (out, or out / 2 for the gated epilogue)
     int gs;                     // quantisation groups per 128 channels (1, or 2 for group 64)
@@ -315,7 +316,6 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     using C = PairCfg<BN>;
     constexpr int kXStages = C::kXStages, kWStages = C::kWStages;
     constexpr uint32_t kHalfX = C::kHalfX, kXStage = C::kXStage;
-    constexpr uint32_t kIdesc = umma_idesc_f16(256, BN);
     constexpr uint32_t kTokenBytes = EPI == kEpiGated ? 32 : 64;       // one token of an epilogue warp's buffer
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -327,6 +327,9 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     const uint32_t go0 = rfull0 + 16 * 8;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* abort = tslot + 1;
+
+    const int bn = C::kSplit ? BN : a.bn;
+    const uint32_t idesc = umma_idesc_f16(256, bn);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_rank(), rank = crank & 1;           // CTA of the cluster, of the pair
@@ -374,7 +377,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 
     // tile -> row blocks of this CTA, first token, first channel stage (of k0 .. k0 + nk - 1)
     auto row_block0 = [&](int tile) { return ((tile % a.mt) * 2 + (int)rank) * 8; };
-    auto token0 = [&](int tile) { return tile / a.mt * BN; };
+    auto token0 = [&](int tile) { return tile / a.mt * bn; };
     auto kstart = [&](int tile) { return k0 + (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
     auto knext = [&](int kb) { return kb + 1 == k0 + nk ? k0 : kb + 1; };
 
@@ -389,7 +392,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         for (int s = 0; s < kWStages; ++s) issued[s] = 0;
         bool ok = true;
         for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
-            const int rb0 = row_block0(tile), n0 = token0(tile) + BN / 2 * (int)rank;
+            const int rb0 = row_block0(tile), n0 = token0(tile) + bn / 2 * (int)rank;
             int kb = kstart(tile);
             for (int i = 0; i < nk; ++i) {
                 const int slot = xs ? px.slot : pw.slot;
@@ -400,7 +403,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 if (xs) {
                     const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, kXStage);
+                        mbar_arrive_expect_tx(bar, (uint32_t)bn * 128);
                         tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
                         tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
                     }
@@ -469,7 +472,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)     // two 64-channel boxes of four MMAs each
-                            umma_f16_ts_pair(tbase, w + kk * 8, b + (uint64_t)((kk >> 2) * (int)(kHalfX >> 4) + (kk & 3) * 2), kIdesc,
+                            umma_f16_ts_pair(tbase, w + kk * 8, b + (uint64_t)((kk >> 2) * (int)(kHalfX >> 4) + (kk & 3) * 2), idesc,
                                              i + kk > 0 ? 1u : 0u);
                         umma_commit_pair(free0 + 8 * s, both);
                     }
@@ -577,7 +580,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             float b = 0.f;
             if (a.bias && row < a.out) b = __half2float(a.bias[EPI == kEpiGated ? col0 + ch + (up ? a.width : 0) : row]);
             // batch j: tokens t0 + 32 j .. + 31, buffer j & 1
-            auto live = [&](int j) { return in_row && t0 + 32 * j < a.T; };
+            const int t_end = min(a.T, token0(tile) + bn);
+            auto live = [&](int j) { return in_row && t0 + 32 * j < t_end; };
             auto load_residual = [&](int j) {             // lane 0, once the buffer's last store has been read
                 mbar_arrive_expect_tx(rbar0 + 8 * (j & 1), kOutBuf);
                 tma_load_2d(buf0 + (j & 1) * kOutBuf, &tm_r, col0, t0 + 32 * j, rbar0 + 8 * (j & 1));
@@ -692,10 +696,18 @@ cudaError_t pair_clusters(int dev, int pairs, int* clusters) {
     return cudaSuccess;
 }
 
+// Tokens of a tile of the 256-token form: the batch in as few tiles as it
+// takes, of equal size in steps of 32 (333 tokens: two tiles of 192, not of 256).
+int balanced_tile(int T) {
+    const int tiles = (T + 255) / 256;
+    return (((T + tiles - 1) / tiles) + 31) / 32 * 32;
+}
+
 // What a product takes in each form, in SM cycles: rounds of tiles that do not
 // fit at once, times a tile's stages and its start and end. The figures are
 // measured (4096 -> 28672 and 14336 -> 4096, 17 to 512 tokens): a stage of the
-// 256-token form 1250 and a tile's change-over 4000; a stage of the split form
+// 256-token form 1250 (less for smaller tiles, down to the dequantisation's
+// 900) and a tile's change-over 4000; a stage of the split form
 // 800, its start, exchange and end 11000, 1500 more with several pairs. Taking
 // the cheaper one, 4096 -> 4096 at 256 tokens runs in the split form (32 tiles
 // of 128 tokens, two pairs each) and 4096 -> 28672 at 256 in the other.
@@ -705,7 +717,8 @@ struct PairPlan {
 };
 template <int BN, int EPI>
 cudaError_t plan_pair(int dev, const PairArgs& a, PairPlan* plan) {
-    const int tiles = a.mt * ((a.T + BN - 1) / BN);
+    const int bn = PairCfg<BN>::kSplit ? BN : balanced_tile(a.T);
+    const int tiles = a.mt * ((a.T + bn - 1) / bn);
     *plan = PairPlan();
     for (int p = 1; p <= (PairCfg<BN>::kSplit ? std::min(kMaxPairs, a.nk) : 1); ++p) {
         int n = 0;
@@ -713,7 +726,7 @@ cudaError_t plan_pair(int dev, const PairArgs& a, PairPlan* plan) {
         if (e != cudaSuccess) return e;
         const long rounds = (tiles + n - 1) / n, stages = (a.nk + p - 1) / p;
         const long cost = PairCfg<BN>::kSplit ? rounds * (stages * 800 + 11000 + (p > 1 ? 1500 : 0))
-                                              : rounds * (stages * 1250 + 4000) + 6000;
+                                              : rounds * (stages * std::max(900, 1250 * bn / 256) + 4000) + 6000;
         if (plan->cost == 0 || cost < plan->cost) {
             plan->cost = cost;
             plan->pairs = p;
@@ -724,7 +737,7 @@ cudaError_t plan_pair(int dev, const PairArgs& a, PairPlan* plan) {
 
 template <int BN, int EPI>
 cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPlan& plan, cudaStream_t s) {
-    a.ntiles = a.mt * ((a.T + BN - 1) / BN);
+    a.ntiles = a.mt * ((a.T + a.bn - 1) / a.bn);
     a.pairs = plan.pairs;
     int clusters = a.ntiles;                               // split form: one tile per cluster
     if (!PairCfg<BN>::kSplit) {
@@ -751,7 +764,7 @@ cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPl
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The operands' tensor maps: X' fp16 [T][in], box 64 channels x BN / 2 tokens,
+// The operands' tensor maps: X' fp16 [T][in], box 64 channels x half a tile's tokens,
 // 128-byte swizzle; codes as uint32 [out/16][in/128 * 256], box 128 channels x
 // 8 row blocks; scales uint32 [out/16][G * 8], box the stage's groups x 8 row
 // blocks; zeros uint8 [out/16][Gp * 8], box two groups x 8 row blocks; Y and
@@ -759,13 +772,14 @@ cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPl
 // the 256-token form). Rows past T or out are read as zeros and not written.
 template <int BN, int EPI>
 cudaError_t encode_and_launch(int dev, const void* Xr, const void* qw, const void* scp, const void* zp, int64_t in,
-                              int group, const PairArgs& a, const PairPlan& plan, cudaStream_t s) {
+                              int group, PairArgs a, const PairPlan& plan, cudaStream_t s) {
+    a.bn = PairCfg<BN>::kSplit ? BN : balanced_tile(a.T);
     const uint64_t G = (uint64_t)(in / group), Gp = G + (G & 1), nrb = (uint64_t)(a.out / 16);
     const uint32_t cols = EPI == kEpiGated ? 16u : 32u;
     CUtensorMap tm[6];
     const bool ok =
         encode_tma_2d(&tm[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Xr, (uint64_t)in, (uint64_t)a.T, (uint64_t)in * 2, 64u,
-                      (uint32_t)BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                      (uint32_t)a.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
         encode_tma_2d(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, (uint64_t)a.nk * 256, nrb, (uint64_t)a.nk * 1024, 256u, 8u,
                       CU_TENSOR_MAP_SWIZZLE_NONE) &&
         encode_tma_2d(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, scp, G * 8, nrb, G * 32, 8u * (uint32_t)a.gs, 8u,

@@ -77,7 +77,8 @@ class RowParallelLinear:
             self.qw, self.sp, self.zp = B.paro_pack_weights(torch.from_numpy(qr), torch.from_numpy(sr),
                                                             torch.from_numpy(zr), device=self.device, group=group)
 
-    def forward(self, X_local, process_group=None):
+    def _sums(self, X_local, process_group):
+        """The ranks' shares added up, fp32 [tokens][out], without the bias."""
         torch = self.torch
         import torch.distributed as dist
         T = X_local.shape[0]
@@ -88,7 +89,17 @@ class RowParallelLinear:
             Yf = torch.zeros((T, self.out_features), dtype=torch.float32, device=self.device)
         if dist.is_available() and dist.is_initialized():
             dist.all_reduce(Yf, op=dist.ReduceOp.SUM, group=process_group)
-        return B.paro_finalize(Yf, self.bias)
+        return Yf
+
+    def forward(self, X_local, process_group=None):
+        return B.paro_finalize(self._sums(X_local, process_group), self.bias)
+
+    def forward_norm(self, X_local, weight, eps: float, residual=None, H=None, process_group=None):
+        """The layer, the residual's addition and the next layer's norm:
+        (Y, H) of paro_rmsnorm on the summed shares (H = fp16(layer + residual),
+        Y its norm), which takes the place of the finalize step, so the layer's
+        own output is never written. H=residual updates it in place."""
+        return B.paro_rmsnorm(self._sums(X_local, process_group), weight, eps, residual=residual, bias=self.bias, H=H)
 
     def close(self):
         if self.rot is not None:
