@@ -19,8 +19,9 @@
 // result does not depend on the batch. A 128-channel group is sixteen
 // neighbouring lanes, so its scale is a four-step shuffle.
 // Measured (fp16 x, residual and H; HBM copy peak 6552 GB/s): 8192 x 4096
-// 45.0 us, 5970 GB/s; 4096 x 5120 with codes 29.3 us, 5000 GB/s; one token of
-// 4096 1.7 us, which is launch and latency. A persistent form with a
+// 43.0 us, 6250 GB/s; 4096 x 5120 with codes 26.6 us (128 channels per scale)
+// and 29.3 us (one scale per row), 5520 and 5000 GB/s; 2048 x 8192 from fp32
+// 27.1 us, 6190 GB/s; one token of 4096 1.6 us, which is launch and latency. A persistent form with a
 // three-deep cp.async ring of rows ran slower (50.2 and 30.0 us): enough CTAs
 // are resident that one's loads cover another's reduction.
 #include <cuda_fp8.h>
@@ -84,7 +85,7 @@ __device__ __forceinline__ NormPlace norm_place(const NormArgs& a) {
     NormPlace p;
     p.lane = threadIdx.x & 31;
     p.warp = threadIdx.x >> 5;
-    p.rw = p.warp / a.wpr;
+    p.rw = a.rows == 1 ? 0 : p.warp / a.wpr;               // (a division costs as much as a vector's arithmetic)
     p.wr = p.warp - p.rw * a.wpr;
     p.t0 = p.wr * 32 + p.lane;                             // first vector of the row, then every tr-th
     p.tr = a.wpr * 32;
@@ -154,7 +155,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, 
             if (OUT == kNormQ8Row) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         }
     }
-    const float rms = 1.f / sqrtf(ss * a.inv_f + a.eps);
+    const float rms = rsqrtf(ss * a.inv_f + a.eps);        // 2 ulp; infinity gives 0
     float inv_row = 0.f;
     if (OUT == kNormQ8Row) {
         const float s = fmaxf(mx * rms / kE4m3Max, kScaleFloor);
@@ -207,8 +208,11 @@ __device__ __forceinline__ void unpack_x(const uint4 (&x)[X32 ? 2 : 1], float v[
 
 }  // namespace
 
+// Registers per thread are held to what keeps as many warps resident as the
+// loads need (two vectors per thread: 48 registers, 4096 x 5120 with codes
+// 26.6 us; 56 took 34.8 us, 40 took 32.1 us).
 template <int VPT, bool X32, int OUT>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+__global__ void __maxnreg__(VPT == 2 ? 48 : VPT == 1 ? 32 : 64) rmsnorm_kernel(const NormArgs a) {
     // the next kernel may launch; it reads nothing of ours before this grid is complete
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int XV = X32 ? 2 : 1;
@@ -319,8 +323,9 @@ cudaError_t launch_rmsnorm(const void* x, bool x_fp32, const void* r, const void
     const int out = !S ? kNormF16 : scale_group ? kNormQ8Group : kNormQ8Row;
     // The split of a row over threads goes by its width alone, so a row's
     // sums have the same order in every batch. One vector per thread up to
-    // 4096 channels, then two (8192 x 4096: 45.0 us with one, 49.6 with two;
-    // 4096 x 5120 in 8 bits: 29.3 us with two, 35.3 with one), then four.
+    // 4096 channels, then two, then four (measured on an earlier build of this
+    // kernel: 8192 x 4096 45.0 us with one and 49.6 with two, 4096 x 5120 in
+    // 8 bits 29.3 us with two and 35.3 with one).
     const int nw = (a.nvec + 31) / 32;                      // warps at one vector per thread
     const int vpt = nw > 64 ? 4 : nw > 16 ? 2 : 1;
     a.wpr = (nw + vpt - 1) / vpt;
