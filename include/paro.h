@@ -223,9 +223,11 @@ typedef enum {
  *   act           a paro_act
  * Y may share memory with the residual only, and only as the same pointer;
  * the workspace shares none with X, the residual or Y (else PARO_ERR_ARG).
- * Other arguments, workspace and errors as paro_linear_ex. Above 128 tokens
+ * Other arguments, workspace and errors as paro_linear_ex. Above 16 tokens
  * the product runs on pairs of SMs (tcgen05 with cta_group::2). The result
- * has the same bits in every call with the same arguments. */
+ * has the same bits in every call with the same arguments. A rotation handle
+ * belongs to the device that was current when it was made, which must be the
+ * current one (else PARO_ERR_ARG). */
 paro_status paro_linear_act(const paro_rot* rot, const void* X_dev,
                             const void* qweight_dev, const void* scales_dev, const void* zeros_dev,
                             const void* bias_dev, const void* residual_dev, int act, int group, void* Y_dev,

@@ -352,12 +352,19 @@ def _bias(bias: Optional[torch.Tensor], n: int) -> Optional[int]:
     return _dev(bias, torch.float16, "bias")
 
 
+def _same_device(X: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != X.device:
+            raise ValueError(f"{name} is on {t.device}, X on {X.device}")
+
+
 def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int, act: str = "none",
                     group: int = 128, bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
                     Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Y = act((X T^-1) w_hat^T + bias) + residual, rounded once; Y may be the residual."""
     a, b = _act(act), _bias(bias, out_features)
     x = _dev(X, torch.float16, "X")
+    _same_device(X, qweight=qw, scales=sp, zeros=zp, bias=bias, workspace=ws)
     T, in_f = X.shape
     shape = (T, out_features)
     r = None if residual is None else _f16(residual, shape, X.get_device(), "residual")
@@ -400,6 +407,7 @@ def paro_linear_gated(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, inte
     from paro_pack_gated, bias [2 inter] (the gate's first)."""
     a, b = _act(act), _bias(bias, 2 * inter_features)
     x = _dev(X, torch.float16, "X")
+    _same_device(X, qweight=qw, scales=sp, zeros=zp, bias=bias, workspace=ws)
     T, in_f = X.shape
     H = _out(H, (T, inter_features), torch.float16, X.device, "H")
     if ws is None:
@@ -444,6 +452,7 @@ class ParoLinear:
                 raise ValueError(f"packed weights of {t.numel()} bytes, {need} needed for this shape and group")
         self._b = _bias(bias, rows)
         self.device = qw.device if device is None else torch.device(device)
+        self._index = qw.get_device()
         self._ws = None
         self._ws_tokens = 0
         self._f = lib().paro_linear_ex
@@ -464,6 +473,8 @@ class ParoLinear:
             Y = torch.empty((T, self.out_features), dtype=torch.float16, device=X.device)
         elif not Y.is_cuda or Y.dtype is not torch.float16 or not Y.is_contiguous() or Y.numel() != T * self.out_features:
             raise TypeError(f"Y must be a contiguous fp16 CUDA tensor [tokens][{self.out_features}]")
+        if X.get_device() != Y.get_device() or X.get_device() != self._index:
+            raise ValueError(f"X on {X.device}, Y on {Y.device}, the layer on {self.device}")
         if T > self._ws_tokens or self._ws is None:
             self._workspace(T)
         if stream is None:
@@ -473,6 +484,9 @@ class ParoLinear:
     def __call__(self, X: torch.Tensor, Y: Optional[torch.Tensor] = None, stream=None,
                  residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         T, Y, sp = self._prepare(X, Y, stream)
+        if _current_device is not None and _current_device() != self._index:   # launch on the layer's device
+            with torch.cuda.device(self._index):
+                return self(X, Y, sp, residual)
         if residual is None and self._a == 0:
             st = self._f(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, self.group, Y.data_ptr(), T,
                          self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
@@ -501,6 +515,9 @@ class ParoGated(ParoLinear):
 
     def __call__(self, X: torch.Tensor, H: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T, H, sp = self._prepare(X, H, stream)
+        if _current_device is not None and _current_device() != self._index:   # launch on the layer's device
+            with torch.cuda.device(self._index):
+                return self(X, H, sp)
         st = self._f_gated(self._h, X.data_ptr(), self._qw, self._sp, self._zp, self._b, self._a, self.group,
                            H.data_ptr(), T, self.in_features, self.out_features, self._ws.data_ptr(), self._ws.numel(), sp)
         if st != PARO_OK:

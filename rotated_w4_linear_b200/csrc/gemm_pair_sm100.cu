@@ -81,7 +81,11 @@ struct PairCfg {
     static constexpr uint32_t kSums = kSplit ? BN * 128 * 4 : 0;       // in the rings' space
     static constexpr uint32_t kBody = kRings > kSums ? kRings : kSums;
     static constexpr int kBars = 4 * kXStages + 2 * kWStages + 3 + 16;
-    static constexpr size_t kSmem = 1024 + (size_t)kBody + 8 * kBars + 16;
+    // Never less than 160 KB: the kernel takes all of an SM's tensor memory, so
+    // a second kernel that wants some must not share the SM with it (two that
+    // each held one SM of a pair would wait for each other)
+    static constexpr size_t kUsed = 1024 + (size_t)kBody + 8 * kBars + 16;
+    static constexpr size_t kSmem = kUsed > 160 * 1024 ? kUsed : 160 * 1024;
     static_assert(BN + 64 * kXStages <= 512, "tensor memory");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -231,9 +235,9 @@ struct PairGated {
 };
 
 // BN < 256: the pairs' sums of this CTA's rows, added in pair order, to the
-// output: tokens [BN pair / pairs, BN (pair + 1) / pairs) of the tile, four rows (gated:
-// four gate and four up rows) of one token per thread and step. A CTA whose
-// rows or tokens lie outside takes no part.
+// output: tokens [BN pair / pairs, BN (pair + 1) / pairs) of the tile, four
+// rows (gated: four gate and four up rows) of one token per thread and step.
+// A CTA whose rows or tokens lie outside takes no part.
 template <int BN, int EPI>
 __device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums, int rb0, int n0, uint32_t rank,
                                                int pair, int pairs) {
@@ -432,9 +436,9 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     mbar_wait((xs ? xfull0 : wfull0) + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
     } else if (warp == 2) {
         if (lane == 0) {
-            // ---- gate: one report per stage to the leader's MMA thread, which
-            // then looks at a single barrier (a look takes about 100 cycles,
-            // and its MMA queue does not hold enough work for three)
+            // ---- gate: one report per stage and CTA to the leader's MMA warp,
+            // which then looks at one barrier instead of three (a look takes
+            // about 100 cycles)
             const uint32_t go_leader0 = map_to_rank(go0, crank & ~1u);
             RingPos<kXStages> p;
             uint32_t tiles = 0;

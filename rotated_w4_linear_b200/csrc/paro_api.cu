@@ -654,6 +654,9 @@ paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const 
     paro_linear_workspace_size(T, in, out, &need);
     if (ws_bytes < need) return fail(PARO_ERR_ARG, "workspace_bytes=%zu < %zu", ws_bytes, need);
     if (epi.kind != paro::kEpiPlain) {
+        int dev = 0;
+        if (r && cudaGetDevice(&dev) == cudaSuccess && dev != r->device)
+            return fail(PARO_ERR_ARG, "rotation prepared on device %d, current device is %d", r->device, dev);
         // the output may be exactly the residual and shares no memory with anything else that is read or written
         const size_t nx = (size_t)T * in * 2, ny = (size_t)T * (epi.kind == paro::kEpiGated ? out / 2 : out) * 2;
         const void* R = epi.residual;
