@@ -13,14 +13,15 @@
 //     few; bound by the weights' way to the tensor cores): one tile per cluster, whose one to four pairs split the channels,
 //     since the row tiles alone would leave most SMs idle; the pairs' sums
 //     meet through distributed shared memory in a fixed order.
-// Per CTA, twenty warps:
-//   warps 0, 19 TMA producers: per stage of 128 channels the CTA's half of the
-//               tokens of X' (two 64-channel boxes, 128-byte swizzle), and the
-//               int4 codes of its 8 row blocks with their scales and zeros,
-//               whose ring is two stages deeper;
-//   warps 3-10  dequantise (w_hat = fp16((q - z) s), as the other kernels do)
-//               into a ring of tensor-memory stages: a warp takes one quarter
-//               of the rows and one half of the stage's channels;
+// Per CTA, twenty warps (BN < 256: twenty-one):
+//   warps 0, 19 (20)  TMA producers: per stage of 128 channels the CTA's half of
+//               the tokens of X' (two 64-channel boxes, 128-byte swizzle), and
+//               the int4 codes of its 8 row blocks with their scales and zeros,
+//               whose ring is deeper;
+//   warps 3-10 (BN < 256: 3-14)  dequantise (w_hat = fp16((q - z) s), as the
+//               other kernels do) into a ring of tensor-memory stages: a warp
+//               takes one quarter of the rows and one half of the stage's
+//               channels (BN < 256: all of every third stage's channels);
 //   warp 2      gate: one lane reports to the pair's leader when its CTA's X'
 //               and w_hat of a stage are there;
 //   warp 1      tensor memory; in the leader the warp issues the MMAs (A from
@@ -31,10 +32,9 @@
 //               into registers (after the second 64 the accumulator is free
 //               for the next tile), then through a 32-token buffer of its own
 //               in shared memory, where the residual has arrived by TMA, to a
-//               TMA store. BN < 256: these warps dequantise every second
-//               stage; then all sixteen put the fp32 sums into shared memory
-//               (the rings' space), and after a cluster barrier all warps add
-//               the pairs' sums, apply the epilogue and store.
+//               TMA store. BN < 256: warps 3-18 put the fp32 sums into shared
+//               memory (the rings' space), and after a cluster barrier all
+//               warps add the pairs' sums, apply the epilogue and store.
 // All waits are bounded (sm100.cuh); a wait that runs out raises the CTA's
 // abort flag, every role stops, what was issued is drained, and the cluster's
 // CTAs meet at the last barrier.
@@ -61,7 +61,6 @@ namespace paro {
 
 namespace {
 
-constexpr int kPairThreads = 640;
 constexpr uint32_t kWCodes = 8 * 1024;                  // 8 row blocks x 128 channels of codes
 constexpr uint32_t kWScales = 8 * 64;                   // 8 row blocks x up to 2 groups x 8 words
 constexpr uint32_t kWStage = kWCodes + kWScales + 128;  // zeros: 8 row blocks x 2 groups x 8 bytes
@@ -73,7 +72,15 @@ constexpr uint32_t kOutBuf = 32 * 64;                   // 32 tokens x 32 rows o
 template <int BN>
 struct PairCfg {
     static constexpr bool kSplit = BN < 256;
-    static constexpr int kXStages = kSplit ? 6 : 4, kWStages = kXStages + 2;
+    // 20 warps, 21 in the split form (a second producer of the weights): one
+    // warp more leaves 80 registers a thread, which the 256-token form's
+    // epilogue does not fit
+    static constexpr int kWProducers = kSplit ? 2 : 1, kThreads = 32 * (19 + kWProducers);
+    static constexpr int kXStages = kSplit ? 6 : 4, kWStages = kSplit ? 12 : 6;
+    // Dequantisation: groups of warps that take turns at the stages. A slot's
+    // uses must all be one group's, for its waits by phase parity.
+    static constexpr int kGroups = kSplit ? 3 : 1, kGroupWarps = kSplit ? 4 : 8;
+    static_assert(kXStages % kGroups == 0 && kWStages % kGroups == 0, "every slot belongs to one group");
     static constexpr uint32_t kHalfX = BN / 2 * 128;    // BN / 2 tokens x 64 channels
     static constexpr uint32_t kXStage = 2 * kHalfX;
     static constexpr uint32_t kOut = kSplit ? 0 : 16 * kOutBuf;
@@ -244,7 +251,7 @@ __device__ __forceinline__ void split_epilogue(const PairArgs& a, uint32_t sums,
     constexpr int kFours = EPI == kEpiGated ? 16 : 32;     // fours per token
     const int t0 = BN * pair / pairs, t1 = min(a.T - n0, BN * (pair + 1) / pairs);
     const int c0 = EPI == kEpiGated ? rb0 * 8 : rb0 * 16;
-    for (int i = threadIdx.x; i < (t1 - t0) * kFours; i += kPairThreads) {
+    for (int i = threadIdx.x; i < (t1 - t0) * kFours; i += PairCfg<BN>::kThreads) {
         const int t = t0 + i / kFours, k = i % kFours;
         // gated: the k-th four gate rows sit in row block k / 2, their up rows eight further on
         const int r = EPI == kEpiGated ? (k >> 1) * 16 + (k & 1) * 4 : 4 * k;
@@ -309,7 +316,7 @@ struct RingPos {
 }  // namespace
 
 template <int BN, int EPI>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(PairCfg<BN>::kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                  const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_z,
                  const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
@@ -349,12 +356,12 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(xfull0 + 8 * s, 1);
             mbar_init(free0 + 8 * s, 1);                  // the MMAs on X' stage and w_hat stage s are done
-            mbar_init(afull0 + 8 * s, 8);                 // this CTA's dequantisation warps
+            mbar_init(afull0 + 8 * s, C::kGroupWarps);    // this CTA's dequantisation warps
             mbar_init(go0 + 8 * s, 2);                    // leader: both CTAs' gates
         }
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull0 + 8 * s, 1);
-            mbar_init(wfree0 + 8 * s, 8);
+            mbar_init(wfree0 + 8 * s, C::kGroupWarps);
         }
         mbar_init(accfull, 1);
         mbar_init(accfree, 8);                            // this CTA's epilogue warps have the sums
@@ -385,24 +392,29 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     auto kstart = [&](int tile) { return k0 + (int)((((uint32_t)(tile % a.mt) * 0x9E3779B1u) >> 16) % (uint32_t)nk); };
     auto knext = [&](int kb) { return kb + 1 == k0 + nk ? k0 : kb + 1; };
 
-    if (warp == 0 || warp == 19) {
-        // ---- TMA producers: X' (warp 0), weights (warp 19). As with the MMAs,
-        // the whole warp walks the stages and one elected lane issues.
+    if (warp == 0 || warp >= 19) {
+        // ---- TMA producers: X' (warp 0), weights (warp 19; BN < 256: warps 19
+        // and 20 in turns, a stage's three loads and waits take one warp 650
+        // cycles). As with the MMAs, the whole warp walks the stages and one
+        // elected lane issues.
         const bool xs = warp == 0;
+        const int w0 = xs ? 0 : warp - 19, step = xs ? 1 : C::kWProducers;
+        static_assert(kWStages % C::kWProducers == 0, "every slot belongs to one warp");
         RingPos<kXStages> px;
         RingPos<kWStages> pw;
-        uint32_t issued[kWStages];                        // loads issued so far per slot (for the drain)
-#pragma unroll
-        for (int s = 0; s < kWStages; ++s) issued[s] = 0;
+        if (w0) pw.next();
+        uint32_t mine = 0;                                // loads issued by this warp
+        int ahead = w0;                                   // stages to the warp's next one, over tile borders
         bool ok = true;
         for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
             const int rb0 = row_block0(tile), n0 = token0(tile) + bn / 2 * (int)rank;
-            int kb = kstart(tile);
-            for (int i = 0; i < nk; ++i) {
+            int i = ahead, kb = kstart(tile) + ahead;
+            if (kb >= k0 + nk) kb -= nk;
+            for (; i < nk; i += step) {
                 const int slot = xs ? px.slot : pw.slot;
                 const uint32_t use = xs ? px.use : pw.use;
                 ok = use == 0 || mbar_wait((xs ? free0 : wfree0) + 8 * slot, (use - 1) & 1, kFaultGemmPair + kFaultTmaWait, abort);
-                ok = __all_sync(0xffffffffu, ok && !*abort);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (xs) {
                     const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
@@ -420,20 +432,25 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                         tma_load_2d(dst + kWCodes, &tm_s, kb * 8 * a.gs, rb0, bar);
                         tma_load_2d(dst + kWCodes + kWScales, &tm_z, (a.gs == 2 ? kb : kb >> 1) * 16, rb0, bar);
                     }
-                    pw.next();
+#pragma unroll
+                    for (int e = 0; e < C::kWProducers; ++e) pw.next();
                 }
                 __syncwarp();
-#pragma unroll
-                for (int t = 0; t < kWStages; ++t)
-                    if (t == slot) issued[t] = use + 1;
-                kb = knext(kb);
+                ++mine;
+                kb += step;
+                if (kb >= k0 + nk) kb -= nk;
+            }
+            ahead = i - nk;
+        }
+        if (*abort) {   // drain: every issued load must land before the CTA exits
+            // the j-th load of this warp went to slot (w0 + step j) mod N
+            const int n = xs ? kXStages : kWStages, per = n / step;
+            for (int t = 0; t < per; ++t) {
+                const uint32_t uses = (mine + (uint32_t)(per - 1 - t)) / (uint32_t)per;   // of its t-th slot
+                if (uses > 0)
+                    mbar_wait((xs ? xfull0 : wfull0) + 8 * (w0 + step * t), (uses - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
             }
         }
-        if (*abort)   // drain: every issued load must land before the CTA exits
-#pragma unroll
-            for (int s = 0; s < kWStages; ++s)
-                if (issued[s] > 0)
-                    mbar_wait((xs ? xfull0 : wfull0) + 8 * s, (issued[s] - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
     } else if (warp == 2) {
         if (lane == 0) {
             // ---- gate: one report per stage and CTA to the leader's MMA warp,
@@ -488,59 +505,67 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (elect_one()) umma_commit_pair(fin, both); // always: arrives once every MMA issued above has completed
             __syncwarp();
         }
-    } else if (C::kSplit || warp < 11) {
-        // ---- dequantisation (BN < 256: two groups of eight warps take turns)
+    } else if (C::kSplit ? warp < 19 : warp < 11) {
+        // ---- dequantisation. BN = 256: eight warps, each a quarter of the
+        // rows and a half of the channels of every stage. BN < 256: groups of
+        // four warps take turns, each warp a quarter of the rows of its stage,
+        // so that a stage's waits are paid once for twice the work (780 SM
+        // cycles a stage with two groups of eight).
         const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
-        const int half = ((warp - 3) >> 2) & 1;           // channels 64 half .. + 63 of a stage
-        // A slot's uses must all be one group's, for its waits by phase parity
-        constexpr int kGroups = C::kSplit ? 2 : 1;
-        static_assert(kXStages % kGroups == 0 && kWStages % kGroups == 0, "every slot belongs to one group");
-        const int group = C::kSplit ? (warp - 3) >> 3 : 0;
+        const int group = C::kGroups > 1 ? (warp - 3) >> 2 : 0;
+        constexpr int kHalves = C::kGroupWarps == 4 ? 2 : 1;
+        const int half0 = kHalves == 2 ? 0 : ((warp - 3) >> 2) & 1;    // first 64-channel half
         const int g = lane >> 2;
         RingPos<kXStages> p;
         RingPos<kWStages> pw;
         bool ok = true;
-        if (group) p.next(), pw.next();
-        for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
+        for (int e = 0; e < group; ++e) p.next(), pw.next();
+        for (int tile = first_tile; ok && group < C::kGroups && tile < a.ntiles; tile += nclusters) {
             int kb = kstart(tile);
-            if (group) kb = knext(kb);
-            for (int i = group; i < nk; i += kGroups) {
+            for (int e = 0; e < group; ++e) kb = knext(kb);
+            for (int i = group; i < nk; i += C::kGroups) {
                 const int s = p.slot;
                 // the tensor-memory stores below are warp-collective: the whole
                 // warp goes on only if every lane saw the stage arrive
                 ok = mbar_wait(wfull0 + 8 * pw.slot, pw.use & 1, kFaultGemmPair + kFaultDequantWait, abort) && !*abort;
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const uint32_t src = sW + pw.slot * kWStage, zsel = a.gs == 2 ? half : kb & 1;
-                uint4 wv[2];
-                uint32_t sw[2], zb[2];
+                const uint32_t src = sW + pw.slot * kWStage;
+                uint4 wv[kHalves][2];
+                uint32_t sw[kHalves][2], zb[kHalves][2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int rbl = 2 * qw + r;
-                    wv[r] = lds128(src + rbl * 1024 + half * 512 + lane * 16);
-                    sw[r] = lds32(src + kWCodes + (rbl * a.gs + (a.gs == 2 ? half : 0)) * 32 + g * 4);
-                    zb[r] = lds8(src + kWCodes + kWScales + rbl * 16 + zsel * 8 + g);
+                for (int h = 0; h < kHalves; ++h) {
+                    const int half = half0 + h, zsel = a.gs == 2 ? half : kb & 1;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int rbl = 2 * qw + r;
+                        wv[h][r] = lds128(src + rbl * 1024 + half * 512 + lane * 16);
+                        sw[h][r] = lds32(src + kWCodes + (rbl * a.gs + (a.gs == 2 ? half : 0)) * 32 + g * 4);
+                        zb[h][r] = lds8(src + kWCodes + kWScales + rbl * 16 + zsel * 8 + g);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(wfree0 + 8 * pw.slot);
                 ok = p.use == 0 || mbar_wait(free0 + 8 * s, (p.use - 1) & 1, kFaultGemmPair + kFaultDequantWait, abort);
                 if (!__all_sync(0xffffffffu, ok && !*abort)) { ok = false; break; }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    uint32_t sc0, sc1, regs[16];
-                    scale_pairs(sw[r], sc0, sc1);
-                    const Zero2 zc = zero_consts(zb[r]);
-                    dequant_word(wv[r].x, zc, sc0, sc1, regs + 0);
-                    dequant_word(wv[r].y, zc, sc0, sc1, regs + 4);
-                    dequant_word(wv[r].z, zc, sc0, sc1, regs + 8);
-                    dequant_word(wv[r].w, zc, sc0, sc1, regs + 12);
-                    tmem_st_16x256b_x4(tA + s * 64 + half * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
-                }
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t sc0, sc1, regs[16];
+                        scale_pairs(sw[h][r], sc0, sc1);
+                        const Zero2 zc = zero_consts(zb[h][r]);
+                        dequant_word(wv[h][r].x, zc, sc0, sc1, regs + 0);
+                        dequant_word(wv[h][r].y, zc, sc0, sc1, regs + 4);
+                        dequant_word(wv[h][r].z, zc, sc0, sc1, regs + 8);
+                        dequant_word(wv[h][r].w, zc, sc0, sc1, regs + 12);
+                        tmem_st_16x256b_x4(tA + s * 64 + (half0 + h) * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
+                    }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(afull0 + 8 * s);
 #pragma unroll
-                for (int e = 0; e < kGroups; ++e) {
+                for (int e = 0; e < C::kGroups; ++e) {
                     kb = knext(kb);
                     p.next();
                     pw.next();
@@ -682,7 +707,7 @@ cudaError_t pair_clusters(int dev, int pairs, int* clusters) {
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 * pairs, 1, 1);
-        cfg.blockDim = dim3(kPairThreads, 1, 1);
+        cfg.blockDim = dim3(PairCfg<BN>::kThreads, 1, 1);
         cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -751,7 +776,7 @@ cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPl
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * (unsigned)(a.pairs * clusters), 1, 1);
-    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.blockDim = dim3(PairCfg<BN>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
