@@ -19,9 +19,9 @@
 //               the int4 codes of its 8 row blocks with their scales and zeros,
 //               whose ring is deeper;
 //   warps 3-10 (BN < 256: 3-14)  dequantise (w_hat = fp16((q - z) s), as the
-//               other kernels do) into a ring of tensor-memory stages: a warp
-//               takes one quarter of the rows and one half of the stage's
-//               channels (BN < 256: all of every third stage's channels);
+//               other kernels do) into a ring of tensor-memory stages: two
+//               (three) groups of four warps take turns, a warp takes one
+//               quarter of the rows of its group's stage;
 //   warp 2      gate: one lane reports to the pair's leader when its CTA's X'
 //               and w_hat of a stage are there;
 //   warp 1      tensor memory; in the leader the warp issues the MMAs (A from
@@ -79,7 +79,7 @@ struct PairCfg {
     static constexpr int kXStages = kSplit ? 6 : 4, kWStages = kSplit ? 12 : 6;
     // Dequantisation: groups of warps that take turns at the stages. A slot's
     // uses must all be one group's, for its waits by phase parity.
-    static constexpr int kGroups = kSplit ? 3 : 1, kGroupWarps = kSplit ? 4 : 8;
+    static constexpr int kGroups = kSplit ? 3 : 2;
     static_assert(kXStages % kGroups == 0 && kWStages % kGroups == 0, "every slot belongs to one group");
     static constexpr uint32_t kHalfX = BN / 2 * 128;    // BN / 2 tokens x 64 channels
     static constexpr uint32_t kXStage = 2 * kHalfX;
@@ -356,12 +356,12 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(xfull0 + 8 * s, 1);
             mbar_init(free0 + 8 * s, 1);                  // the MMAs on X' stage and w_hat stage s are done
-            mbar_init(afull0 + 8 * s, C::kGroupWarps);    // this CTA's dequantisation warps
+            mbar_init(afull0 + 8 * s, 4);                 // the dequantisation warps of one group
             mbar_init(go0 + 8 * s, 2);                    // leader: both CTAs' gates
         }
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull0 + 8 * s, 1);
-            mbar_init(wfree0 + 8 * s, C::kGroupWarps);
+            mbar_init(wfree0 + 8 * s, 4);
         }
         mbar_init(accfull, 1);
         mbar_init(accfree, 8);                            // this CTA's epilogue warps have the sums
@@ -506,15 +506,11 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             __syncwarp();
         }
     } else if (C::kSplit ? warp < 19 : warp < 11) {
-        // ---- dequantisation. BN = 256: eight warps, each a quarter of the
-        // rows and a half of the channels of every stage. BN < 256: groups of
-        // four warps take turns, each warp a quarter of the rows of its stage,
-        // so that a stage's waits are paid once for twice the work (780 SM
-        // cycles a stage with two groups of eight).
+        // ---- dequantisation: groups of four warps take turns at the stages,
+        // each warp a quarter of the rows of its stage, so that a stage's waits
+        // are paid once for its 16 KB of w_hat
         const int qw = warp & 3;                          // tensor-memory lanes 32 qw .. 32 qw + 31
-        const int group = C::kGroups > 1 ? (warp - 3) >> 2 : 0;
-        constexpr int kHalves = C::kGroupWarps == 4 ? 2 : 1;
-        const int half0 = kHalves == 2 ? 0 : ((warp - 3) >> 2) & 1;    // first 64-channel half
+        const int group = (warp - 3) >> 2;
         const int g = lane >> 2;
         RingPos<kXStages> p;
         RingPos<kWStages> pw;
@@ -530,17 +526,21 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 ok = mbar_wait(wfull0 + 8 * pw.slot, pw.use & 1, kFaultGemmPair + kFaultDequantWait, abort) && !*abort;
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const uint32_t src = sW + pw.slot * kWStage;
-                uint4 wv[kHalves][2];
-                uint32_t sw[kHalves][2], zb[kHalves][2];
+                const bool two = a.gs == 2;               // a scale and a zero for each half of the channels
+                uint4 wv[2][2];                           // [half][row block of the two]
+                uint32_t sw[2][2], zb[2][2];
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    const int half = half0 + h, zsel = a.gs == 2 ? half : kb & 1;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int rbl = 2 * qw + r;
-                        wv[h][r] = lds128(src + rbl * 1024 + half * 512 + lane * 16);
-                        sw[h][r] = lds32(src + kWCodes + (rbl * a.gs + (a.gs == 2 ? half : 0)) * 32 + g * 4);
-                        zb[h][r] = lds8(src + kWCodes + kWScales + rbl * 16 + zsel * 8 + g);
+                for (int r = 0; r < 2; ++r) {
+                    const int rbl = 2 * qw + r;
+                    const uint32_t sc = src + kWCodes + (rbl * a.gs) * 32 + g * 4;
+                    const uint32_t z = src + kWCodes + kWScales + rbl * 16 + g;
+                    wv[0][r] = lds128(src + rbl * 1024 + lane * 16);
+                    wv[1][r] = lds128(src + rbl * 1024 + 512 + lane * 16);
+                    sw[0][r] = lds32(sc);
+                    zb[0][r] = lds8(z + (two ? 0 : (kb & 1) * 8));
+                    if (two) {
+                        sw[1][r] = lds32(sc + 32);
+                        zb[1][r] = lds8(z + 8);
                     }
                 }
                 __syncwarp();
@@ -548,18 +548,23 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 ok = p.use == 0 || mbar_wait(free0 + 8 * s, (p.use - 1) & 1, kFaultGemmPair + kFaultDequantWait, abort);
                 if (!__all_sync(0xffffffffu, ok && !*abort)) { ok = false; break; }
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h)
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t sc0, sc1, regs[16];
+                    scale_pairs(sw[0][r], sc0, sc1);
+                    Zero2 zc = zero_consts(zb[0][r]);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        uint32_t sc0, sc1, regs[16];
-                        scale_pairs(sw[h][r], sc0, sc1);
-                        const Zero2 zc = zero_consts(zb[h][r]);
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1 && two) {
+                            scale_pairs(sw[1][r], sc0, sc1);
+                            zc = zero_consts(zb[1][r]);
+                        }
                         dequant_word(wv[h][r].x, zc, sc0, sc1, regs + 0);
                         dequant_word(wv[h][r].y, zc, sc0, sc1, regs + 4);
                         dequant_word(wv[h][r].z, zc, sc0, sc1, regs + 8);
                         dequant_word(wv[h][r].w, zc, sc0, sc1, regs + 12);
-                        tmem_st_16x256b_x4(tA + s * 64 + (half0 + h) * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
+                        tmem_st_16x256b_x4(tA + s * 64 + h * 32 + ((uint32_t)(32 * qw + 16 * r) << 16), regs);
                     }
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
