@@ -171,8 +171,9 @@ paro_status paro_linear_workspace_size(int64_t tokens, int64_t in_features, int6
  * as a programmatic dependent launch of it (its weight loads start before the
  * rotation has finished). tokens <= 16: the int4 decode kernel (warp MMAs fed
  * by in-register dequantisation, split-k reduced through distributed shared
- * memory inside a thread-block cluster); larger batches: the tensor-core
- * GEMM (w_hat dequantised into tensor memory, X T^-1 tiles by TMA, 64/128/256
+ * memory inside a thread-block cluster), for in_features up to 81920 (40960
+ * above eight tokens); larger batches and wider layers: the tensor-core GEMM
+ * (w_hat dequantised into tensor memory, X T^-1 tiles by TMA, 64/128/256
  * tokens per tile). */
 paro_status paro_linear(const paro_rot* rot, const void* X_dev,
                         const void* qweight_dev, const void* scales_dev, const void* zeros_dev,
@@ -337,9 +338,11 @@ paro_status paro_q8_expand(const void* Q_dev, const float* scales_dev, int scale
  * The rotated activations X T^-1 go to a 1 MiB static device array that the
  * library holds on every device that loads it until the process exits, so
  * tokens * in_features * 2 must not exceed 1 MiB (else PARO_ERR_ARG; e.g. 16
- * tokens x 32768 channels). Every call shares that array and it keeps the
- * last call's contents (nothing in it needs clearing); calls that overlap on
- * the GPU race on it, so serialise them (one stream, or events).
+ * tokens x 32768 channels), and above eight tokens in_features must not
+ * exceed 40960 (81920 up to eight; else PARO_ERR_UNSUPPORTED). Every call
+ * shares that array and it keeps the last call's contents (nothing in it needs
+ * clearing); calls that overlap on the GPU race on it, so serialise them (one
+ * stream, or events).
  * The first call on a device looks up the array's device address
  * (cudaGetSymbolAddress) once for that device; make that first call before
  * any stream capture. Arguments are those of paro_linear without the

@@ -516,10 +516,11 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         RingPos<kWStages> pw;
         bool ok = true;
         for (int e = 0; e < group; ++e) p.next(), pw.next();
+        int ahead = group;                                // stages to the group's next one, over tile borders
         for (int tile = first_tile; ok && group < C::kGroups && tile < a.ntiles; tile += nclusters) {
-            int kb = kstart(tile);
-            for (int e = 0; e < group; ++e) kb = knext(kb);
-            for (int i = group; i < nk; i += C::kGroups) {
+            int i = ahead, kb = kstart(tile) + ahead;
+            if (kb >= k0 + nk) kb -= nk;
+            for (; i < nk; i += C::kGroups) {
                 const int s = p.slot;
                 // the tensor-memory stores below are warp-collective: the whole
                 // warp goes on only if every lane saw the stage arrive
@@ -576,6 +577,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                     pw.next();
                 }
             }
+            ahead = i - nk;
         }
         if (C::kSplit) {
             // ---- the pair's sums into shared memory, fp32 [token][128 rows],

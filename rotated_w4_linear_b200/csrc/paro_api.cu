@@ -58,6 +58,11 @@ paro_status check_device() {
     return PARO_OK;
 }
 
+// Whether the decode kernel has a plan for this width: at most 16 CTAs split
+// the 128-channel groups, each holding the tokens of at most 40 of them (20
+// above eight tokens) in shared memory.
+bool decode_fits(int64_t T, int64_t in) { return T <= 16 && in / 128 <= 16 * (T > 8 ? 20 : 40); }
+
 paro_status check_shape(int64_t in, int64_t out) {
     if (in <= 0 || in % 128) return fail(PARO_ERR_ARG, "in_features=%lld must be a positive multiple of 128", (long long)in);
     if (out <= 0 || out % 16) return fail(PARO_ERR_ARG, "out_features=%lld must be a positive multiple of 16", (long long)out);
@@ -163,6 +168,8 @@ paro_status paro_linear_noalloc(const paro_rot* r, const void* X, const void* qw
     if ((size_t)T * (size_t)in * 2 > paro::noalloc_scratch_bytes())
         return fail(PARO_ERR_ARG, "tokens x in_features x 2 = %zu bytes exceeds the %zu-byte static scratch",
                     (size_t)T * (size_t)in * 2, paro::noalloc_scratch_bytes());
+    if (!decode_fits(T, in))
+        return fail(PARO_ERR_UNSUPPORTED, "in_features=%lld is too wide for a decode batch of %lld", (long long)in, (long long)T);
     if (r && r->dev.in != in) return fail(PARO_ERR_ARG, "rotation prepared for in=%lld, layer has in=%lld", (long long)r->dev.in, (long long)in);
     if (r && r->dev.group != 128) return fail(PARO_ERR_UNSUPPORTED, "this entry point serves group 128");
     if (!X || !qw || !sp || !zp || !Y) return fail(PARO_ERR_ARG, "null pointer");
@@ -671,7 +678,7 @@ paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const paro::RotDev* rd = r ? &r->dev : nullptr;
     cudaError_t e;
-    if (T <= 16) {   // decode rotation kernel into ws, then the int4 decode kernel
+    if (decode_fits(T, in)) {   // decode rotation kernel into ws, then the int4 decode kernel
         e = paro::launch_gemv(rd, X, qw, sp, zp, bias, Y, T, in, out, fmt_group, ws, s, y_fp32, epi);
         return e == cudaSuccess ? PARO_OK : cuda_fail(e, "decode launch");
     }

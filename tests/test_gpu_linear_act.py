@@ -97,6 +97,7 @@ def test_group_sizes(B, T, group, rotated):
     (40, 14336, 4096), (100, 4096, 6144), (77, 2560, 9744),   # prefill, split channels
     (200, 4096, 28672), (256, 4096, 4096), (500, 9728, 2560),
     (2048, 4096, 4096), (1000, 14336, 2576), (300, 5120, 34832),
+    (2000, 384, 8192), (3000, 128, 4096), (1500, 640, 9728),  # an odd number of stages in each of a cluster's tiles
 ])
 def test_layer_sizes(B, T, n_in, n_out):
     L = Layer(B, T, n_in, n_out, seed=3, bias=False)
@@ -300,6 +301,72 @@ def test_prepared_layers_and_side_stream(B):
     gat(L.x, h, stream=st)
     st.synchronize()
     assert torch.equal(y, want_y) and torch.equal(h, want_h)
+
+
+@pytest.mark.parametrize("T", [3, 16, 50, 128, 300])
+def test_rows_behind_the_batch_stay(B, T):
+    L = Layer(B, T, 512, 272, seed=T)
+    G = B.paro_pack_gated(L.q, L.s, L.z)
+    y = torch.full((T + 40, 272), 7.0, dtype=torch.float16, device="cuda")
+    h = torch.full((T + 40, 136), 7.0, dtype=torch.float16, device="cuda")
+    B.paro_linear_act(L.rot, L.x, *L.packed, 272, act="silu", residual=L.residual, Y=y[:T])
+    B.paro_linear_gated(L.rot, L.x, *G, 136, H=h[:T])
+    assert bool((y[T:] == 7).all()) and bool((h[T:] == 7).all())
+    close(y[:T], *R.linear_act(L.xr(), L.w, "silu", None, L.residual))
+
+
+@pytest.mark.parametrize("T", [4, 30, 140])
+def test_bias_at_any_two_byte_address(B, T):
+    L = Layer(B, T, 384, 80, seed=T)
+    G = B.paro_pack_gated(L.q, L.s, L.z)
+    moved = torch.empty(81, dtype=torch.float16, device="cuda")
+    moved[1:] = L.bias
+    assert torch.equal(B.paro_linear_act(L.rot, L.x, *L.packed, 80, act="gelu", bias=moved[1:]),
+                       B.paro_linear_act(L.rot, L.x, *L.packed, 80, act="gelu", bias=L.bias))
+    assert torch.equal(B.paro_linear_gated(L.rot, L.x, *G, 40, bias=moved[1:]),
+                       B.paro_linear_gated(L.rot, L.x, *G, 40, bias=L.bias))
+
+
+@pytest.mark.parametrize("T,n_in", [(9, 41088), (8, 82048), (40, 82048)])
+def test_layers_wider_than_the_decode_kernel_splits(B, T, n_in):
+    """Above 16 k-chunks of 20 (40) groups a decode batch takes the prefill kernels."""
+    L = Layer(B, T, n_in, 48, seed=T, K=1)
+    L.s.mul_(0.1)
+    L.packed, L.w = B.paro_pack_weights(L.q, L.s, L.z), R.w_hat(L.q, L.s, L.z, 128)
+    close(B.paro_linear_act(L.rot, L.x, *L.packed, 48, bias=L.bias, residual=L.residual),
+          *R.linear_act(L.xr(), L.w, "none", L.bias, L.residual))
+    close(B.paro_linear_gated(L.rot, L.x, *B.paro_pack_gated(L.q, L.s, L.z), 24), *R.gated(L.xr(), L.w, "silu"))
+    close(B.paro_linear(L.rot, L.x, *L.packed, 48), *R.linear_act(L.xr(), L.w, "none"))
+
+
+def test_outputs_beyond_32_bits(B):
+    T, n_in, n_out = 66000, 128, 32768                      # 2.16e9 outputs
+    L = Layer(B, 64, n_in, n_out, rotated=False, bias=False)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, n_in, device="cuda", generator=gen).half()
+    y = torch.empty(T, n_out, dtype=torch.float16, device="cuda").normal_(generator=gen)
+    rows = [0, 32767, 65535, 65536, T - 1]
+    before = y[rows].clone()
+    B.paro_linear_act(None, x, *L.packed, n_out, act="relu", residual=y, Y=y)
+    close(y[rows], *R.linear_act(x[rows], L.w, "relu", None, before))
+
+
+def test_blocks_on_two_streams_at_once(B):
+    """Calls in flight together, each with its own workspace and outputs."""
+    L = Layer(B, 200, 1024, 2048, seed=4)
+    G = B.paro_pack_gated(L.q, L.s, L.z)
+    want_y = B.paro_linear_act(L.rot, L.x, *L.packed, 2048, residual=L.residual)
+    want_h = B.paro_linear_gated(L.rot, L.x[:50], *G, 1024)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [B.workspace(200, 1024, 2048) for _ in streams]
+    ys, hs = [torch.empty_like(want_y) for _ in range(20)], [torch.empty_like(want_h) for _ in range(20)]
+    torch.cuda.synchronize()
+    for k in range(20):
+        B.paro_linear_act(L.rot, L.x, *L.packed, 2048, residual=L.residual, Y=ys[k], ws=ws[0], stream=streams[0])
+        B.paro_linear_gated(L.rot, L.x[:50], *G, 1024, H=hs[k], ws=ws[1], stream=streams[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want_y) for y in ys) and all(torch.equal(h, want_h) for h in hs)
 
 
 def test_empty_batches_and_binding_refusals(B):

@@ -127,3 +127,10 @@ def test_gated_widths(L):
     refused(L, L.paro_pack_gated(P[0], P[1], P[2], 250, 32, 128, P[3], P[4], P[5], None), ARG, "in_features")
     refused(L, L.paro_pack_gated(P[0], P[1], P[2], 256, 32, 32, P[3], P[4], P[5], None), UNSUPPORTED, "group")
     refused(L, L.paro_pack_gated(P[0], P[1], P[2], 256, 32, 128, P[3] + 8, P[4], P[5], None), ARG, "aligned")
+
+
+def test_static_scratch_refuses_what_the_decode_kernel_has_no_plan_for(L):
+    """41088 channels at 12 tokens fit the scratch but not sixteen k-chunks of
+    20 groups: refused, where the planner once divided by its empty plan."""
+    assert L.paro_linear_noalloc(None, P[0], P[1], P[2], P[3], P[4], 12, 41088, 64, None) == UNSUPPORTED
+    assert b"too wide" in L.paro_last_error()
