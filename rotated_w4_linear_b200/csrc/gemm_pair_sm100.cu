@@ -39,10 +39,14 @@
 // abort flag, every role stops, what was issued is drained, and the cluster's
 // CTAs meet at the last barrier.
 //
-// What it does per stage (128 rows x 128 channels x 256 tokens per CTA, SM
-// cycles, 4096 -> 28672): the tensor cores need 1024, the kernel takes 1191;
-// with a cluster-scope release by each dequantisation warp it took 1766, with
-// the MMAs issued from a one-lane branch 1246.
+// A stage (128 rows x 128 channels x 256 tokens per CTA) needs 1024 SM cycles
+// of the tensor cores. On the way (4096 -> 28672): 1766 with a cluster-scope
+// release by each dequantisation warp, 1290 with one reporter per CTA, 1191
+// with the MMAs issued from a converged warp; loads issued the same way and
+// the dequantisation in groups of four warps took another 12% off the time,
+// which is then the power limit's: 1455 us for 4096 -> 2 x 14336 at 8192 tokens
+// (1320 TFLOP/s at 1.2-1.35 GHz), 341 us and the tensor pipe 85% busy at 2048.
+// BN = 64: 14336 -> 4096 at 64 tokens 19.8 us (one CTA per tile, unsplit: 94).
 //
 // A token's result does not depend on its place in the batch: the order of the
 // channels goes by the row tile and the split alone.
