@@ -568,13 +568,23 @@ def paro_linear_noalloc(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
     return Y
 
 
-def _f16(t: torch.Tensor, shape, device: int, name: str) -> int:
-    """Data pointer of a contiguous fp16 tensor of this shape on CUDA device `device`."""
-    if t.dtype is not torch.float16 or not t.is_cuda or not t.is_contiguous():
-        _dev(t, torch.float16, name)                        # says which of the three it is
-    if t.shape != shape or t.get_device() != device:
-        raise ValueError(f"{name} must be {list(shape)} on cuda:{device}, got {list(t.shape)} on {t.device}")
-    return t.data_ptr()
+def _f16(t: torch.Tensor, shape, device: int, name: str, dtype: torch.dtype = torch.float16) -> int:
+    """Data pointer of a contiguous fp16 (or `dtype`) tensor of this shape on CUDA device `device`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)                                    # says what is wrong, if not the place or the shape
+    raise ValueError(f"{name} must be {list(shape)} on cuda:{device}, got {list(t.shape)} on {t.device}")
+
+
+def _launch(fn, device: int, stream, *args) -> int:
+    """fn(*args, raw stream) with `device` current, on the given stream or
+    that device's current one."""
+    if _current_device is None or _current_device() != device:
+        with torch.cuda.device(device):
+            return fn(*args, _stream(stream, torch.device("cuda", device)))
+    if stream is None and _raw_stream is not None:
+        return fn(*args, _raw_stream(device))
+    return fn(*args, _stream(stream, torch.device("cuda", device)))
 
 
 def _norm_args(X, weight, residual, bias, H):
@@ -582,9 +592,9 @@ def _norm_args(X, weight, residual, bias, H):
     is allocated when a residual, a bias or fp32 sums make it differ from X."""
     if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in (torch.float16, torch.float32):
         raise TypeError("X must be a [tokens][features] fp16 or fp32 CUDA tensor")
-    x = _dev(X, X.dtype, "X")
     x32 = X.dtype is torch.float32
     shape, dev = X.shape, X.get_device()
+    x = _dev(X, X.dtype, "X")
     row = shape[1:]
     if H is None and (residual is not None or bias is not None or x32):
         H = torch.empty(shape, dtype=torch.float16, device=X.device)
@@ -615,9 +625,8 @@ def paro_rmsnorm(X: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     shape, args, h, H = _norm_args(X, weight, residual, bias, H)
     if Y is None:
         Y = torch.empty(shape, dtype=torch.float16, device=X.device)
-    y = _f16(Y, shape, X.get_device(), "Y")
-    with _on(X.device):
-        st = lib().paro_rmsnorm(*args, eps, h, y, *shape, _stream(stream, X.device))
+    dev = X.get_device()
+    st = _launch(lib().paro_rmsnorm, dev, stream, *args, eps, h, _f16(Y, shape, dev, "Y"), *shape)
     if st != PARO_OK:
         _check("paro_rmsnorm", st)
     return Y, H
@@ -631,11 +640,15 @@ def paro_rmsnorm_q8(X: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     (scale_group 0: one scale per row)."""
     shape, args, h, H = _norm_args(X, weight, residual, bias, H)
     T, F = shape
-    Y = _out(Y, shape, torch.float8_e4m3fn, X.device, "Y")
-    S = _out(S, (T, -(-F // 128) if scale_group else 1), torch.float32, X.device, "S")
-    with _on(X.device):
-        _check("paro_rmsnorm_q8", lib().paro_rmsnorm_q8(*args, eps, scale_group, h, Y.data_ptr(), S.data_ptr(), T, F,
-                                                        _stream(stream, X.device)))
+    scales, dev = (T, -(-F // 128) if scale_group else 1), X.get_device()
+    if Y is None:
+        Y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=X.device)
+    if S is None:
+        S = torch.empty(scales, dtype=torch.float32, device=X.device)
+    st = _launch(lib().paro_rmsnorm_q8, dev, stream, *args, eps, scale_group, h,
+                 _f16(Y, shape, dev, "Y", torch.float8_e4m3fn), _f16(S, scales, dev, "S", torch.float32), T, F)
+    if st != PARO_OK:
+        _check("paro_rmsnorm_q8", st)
     return Y, S, H
 
 

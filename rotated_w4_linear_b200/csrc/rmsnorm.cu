@@ -19,9 +19,9 @@
 // result does not depend on the batch. A 128-channel group is sixteen
 // neighbouring lanes, so its scale is a four-step shuffle.
 // Measured (fp16 x, residual and H; HBM copy peak 6552 GB/s): 8192 x 4096
-// 43.0 us, 6250 GB/s; 4096 x 5120 with codes 26.6 us (128 channels per scale)
+// 42.0 us, 6390 GB/s; 4096 x 5120 with codes 26.6 us (128 channels per scale)
 // and 29.3 us (one scale per row), 5520 and 5000 GB/s; 2048 x 8192 from fp32
-// 27.1 us, 6190 GB/s; one token of 4096 1.6 us, which is launch and latency. A persistent form with a
+// 27.1 us, 6190 GB/s; one token of 4096 1.5 us, which is launch and latency. A persistent form with a
 // three-deep cp.async ring of rows ran slower (50.2 and 30.0 us): enough CTAs
 // are resident that one's loads cover another's reduction.
 #include <cuda_fp8.h>
@@ -322,12 +322,13 @@ cudaError_t launch_rmsnorm(const void* x, bool x_fp32, const void* r, const void
     a.eps = eps;
     const int out = !S ? kNormF16 : scale_group ? kNormQ8Group : kNormQ8Row;
     // The split of a row over threads goes by its width alone, so a row's
-    // sums have the same order in every batch. One vector per thread up to
-    // 4096 channels, then two, then four (measured on an earlier build of this
-    // kernel: 8192 x 4096 45.0 us with one and 49.6 with two, 4096 x 5120 in
-    // 8 bits 29.3 us with two and 35.3 with one).
+    // sums have the same order in every batch: one vector per thread up to 11
+    // warps, then two, then four where 1024 threads would not do (8192 x 4096:
+    // 42.0 us with two, 43.0 with one; 4096 x 5120 with codes 26.6 with two,
+    // 30.0 with one, 31.4 with four; 8192 x 2560 from fp32 32.8 with one, 34.1
+    // with two).
     const int nw = (a.nvec + 31) / 32;                      // warps at one vector per thread
-    const int vpt = nw > 64 ? 4 : nw > 16 ? 2 : 1;
+    const int vpt = nw > 64 ? 4 : nw > 11 ? 2 : 1;
     a.wpr = (nw + vpt - 1) / vpt;
     a.rows = T > 296 && a.wpr < 8 ? 8 / a.wpr : 1;
     return vpt == 4 ? launch_norm_v<4>(a, x_fp32, out, s)
