@@ -245,6 +245,17 @@ def workspace(tokens: int, in_features: int, out_features: int, device=None) -> 
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
+def _scratch(tokens: int, in_features: int, out_features: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream` (None: the current one). Not
+    filled (a fill on the current stream would race with a call on another),
+    and not handed out again before that stream has passed the call."""
+    n = paro_linear_workspace_size(tokens, in_features, out_features)
+    t = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device))
+    return t
+
+
 def paro_linear(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int,
                 Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     T, in_f = X.shape
@@ -370,7 +381,7 @@ def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fe
     r = None if residual is None else _f16(residual, shape, X.get_device(), "residual")
     Y = _out(Y, shape, torch.float16, X.device, "Y")
     if ws is None:
-        ws = workspace(T, in_f, out_features, X.device)
+        ws = _scratch(T, in_f, out_features, X.device, stream)
     with _on(X.device):
         _check("paro_linear_act", lib().paro_linear_act(
             rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
@@ -411,7 +422,7 @@ def paro_linear_gated(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, inte
     T, in_f = X.shape
     H = _out(H, (T, inter_features), torch.float16, X.device, "H")
     if ws is None:
-        ws = workspace(T, in_f, 2 * inter_features, X.device)
+        ws = _scratch(T, in_f, 2 * inter_features, X.device, stream)
     with _on(X.device):
         _check("paro_linear_gated", lib().paro_linear_gated(
             rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
@@ -426,11 +437,11 @@ class ParoLinear:
     here; a call checks only X, Y and the residual and hands raw pointers to
     the same C entry points as paro_linear_ex and paro_linear_act (the latter
     with an activation or a residual). The workspace is owned by the object
-    and grows with the largest batch seen, so calls on one object must not
-    overlap on the GPU (one stream, or events), as for paro_linear's
-    workspace; a CUDA graph that captured a call keeps using the workspace of
-    that time, so the object must outlive the graph and see its largest batch
-    before the capture. The object keeps references to the tensors it was
+    and grows with the largest batch seen (at least twofold; outgrown ones are
+    kept, since a captured CUDA graph goes on using the one of its time), so
+    calls on one object must not overlap on the GPU (one stream, or events),
+    as for paro_linear's workspace, and the object must outlive the graphs
+    that captured it. The object keeps references to the tensors it was
     given."""
 
     _width_factor = 1                                   # rows of the weights per output column
@@ -454,14 +465,16 @@ class ParoLinear:
         self.device = qw.device if device is None else torch.device(device)
         self._index = qw.get_device()
         self._ws = None
+        self._kept = []                                    # outgrown workspaces
         self._ws_tokens = 0
         self._f = lib().paro_linear_ex
         self._f_act = lib().paro_linear_act
 
     def _workspace(self, T: int) -> None:
         if T > self._ws_tokens or self._ws is None:
-            self._ws = workspace(T, self.in_features, self._width_factor * self.out_features, self.device)
-            self._ws_tokens = T
+            self._kept.append(self._ws)
+            self._ws_tokens = max(T, 2 * self._ws_tokens)
+            self._ws = _scratch(self._ws_tokens, self.in_features, self._width_factor * self.out_features, self.device, None)
 
     def _prepare(self, X, Y, stream):
         """(tokens, Y, raw stream) of a call, after its checks."""

@@ -369,6 +369,47 @@ def test_blocks_on_two_streams_at_once(B):
     assert all(torch.equal(y, want_y) for y in ys) and all(torch.equal(h, want_h) for h in hs)
 
 
+def test_side_stream_calls_without_a_workspace(B):
+    """Scratch that a call allocates itself is neither filled on another stream
+    nor handed out again while the call's stream still uses it."""
+    L = Layer(B, 300, 1024, 512, seed=6)
+    G = B.paro_pack_gated(L.q, L.s, L.z)
+    want_y = B.paro_linear_act(L.rot, L.x, *L.packed, 512, residual=L.residual)
+    want_h = B.paro_linear_gated(L.rot, L.x, *G, 256)
+    st = torch.cuda.Stream()
+    ys, hs = [torch.empty_like(want_y) for _ in range(30)], [torch.empty_like(want_h) for _ in range(30)]
+    torch.cuda.synchronize()
+    n = B.paro_linear_workspace_size(300, 1024, 512)
+    for k in range(30):
+        B.paro_linear_act(L.rot, L.x, *L.packed, 512, residual=L.residual, Y=ys[k], stream=st)
+        torch.full((n,), 255, dtype=torch.uint8, device="cuda")     # would land in freed scratch: NaN in X'
+        B.paro_linear_gated(L.rot, L.x, *G, 256, H=hs[k], stream=st.cuda_stream)
+        torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want_y) for y in ys) and all(torch.equal(h, want_h) for h in hs)
+
+
+def test_a_captured_call_survives_a_larger_batch(B):
+    """A graph goes on using the workspace it was captured with after the
+    prepared layer has grown another."""
+    L = Layer(B, 300, 1024, 512, seed=7)
+    layer = B.ParoLinear(L.rot, *L.packed, 1024, 512, act="silu")
+    x = L.x[:40].clone()
+    want = layer(x)
+    y = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(x, y)
+    big = layer(L.x)                                        # outgrows the captured workspace
+    junk = [torch.full((x.numel() * 2,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(5):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    assert torch.equal(big, layer(L.x)) and all(bool((j == 255).all()) for j in junk)
+
+
 def test_empty_batches_and_binding_refusals(B):
     L = Layer(B, 4, 256, 64, seed=1)
     G = B.paro_pack_gated(L.q, L.s, L.z)
