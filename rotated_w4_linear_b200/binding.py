@@ -245,15 +245,23 @@ def workspace(tokens: int, in_features: int, out_features: int, device=None) -> 
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream` (None: the current one),
+    allocated as that stream's memory: one of the current stream's could still
+    be in use there by a tensor freed before, and could be handed out there
+    again before the call has passed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(tokens: int, in_features: int, out_features: int, device, stream) -> torch.Tensor:
-    """A workspace for one call on `stream` (None: the current one). Not
-    filled (a fill on the current stream would race with a call on another),
-    and not handed out again before that stream has passed the call."""
+    """A workspace for one call on `stream`, not filled."""
     n = paro_linear_workspace_size(tokens, in_features, out_features)
-    t = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device))
-    return t
+    return _empty(max(n, 16), torch.uint8, device, stream)
 
 
 def paro_linear(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int,
@@ -379,7 +387,7 @@ def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fe
     T, in_f = X.shape
     shape = (T, out_features)
     r = None if residual is None else _f16(residual, shape, X.get_device(), "residual")
-    Y = _out(Y, shape, torch.float16, X.device, "Y")
+    Y = _out(Y, shape, torch.float16, X.device, "Y", stream)
     if ws is None:
         ws = _scratch(T, in_f, out_features, X.device, stream)
     with _on(X.device):
@@ -420,7 +428,7 @@ def paro_linear_gated(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, inte
     x = _dev(X, torch.float16, "X")
     _same_device(X, qweight=qw, scales=sp, zeros=zp, bias=bias, workspace=ws)
     T, in_f = X.shape
-    H = _out(H, (T, inter_features), torch.float16, X.device, "H")
+    H = _out(H, (T, inter_features), torch.float16, X.device, "H", stream)
     if ws is None:
         ws = _scratch(T, in_f, 2 * inter_features, X.device, stream)
     with _on(X.device):
@@ -470,11 +478,13 @@ class ParoLinear:
         self._f = lib().paro_linear_ex
         self._f_act = lib().paro_linear_act
 
-    def _workspace(self, T: int) -> None:
+    def _workspace(self, T: int, stream=None) -> None:
         if T > self._ws_tokens or self._ws is None:
-            self._kept.append(self._ws)
-            self._ws_tokens = max(T, 2 * self._ws_tokens)
-            self._ws = _scratch(self._ws_tokens, self.in_features, self._width_factor * self.out_features, self.device, None)
+            if self._ws is not None:
+                self._kept.append(self._ws)
+            tokens = max(T, 2 * self._ws_tokens)
+            self._ws = _scratch(tokens, self.in_features, self._width_factor * self.out_features, self.device, stream)
+            self._ws_tokens = tokens
 
     def _prepare(self, X, Y, stream):
         """(tokens, Y, raw stream) of a call, after its checks."""
@@ -483,13 +493,13 @@ class ParoLinear:
                 or X.shape[1] != self.in_features:
             raise TypeError(f"X must be a contiguous fp16 CUDA tensor [tokens][{self.in_features}]")
         if Y is None:
-            Y = torch.empty((T, self.out_features), dtype=torch.float16, device=X.device)
+            Y = _empty((T, self.out_features), torch.float16, X.device, stream)
         elif not Y.is_cuda or Y.dtype is not torch.float16 or not Y.is_contiguous() or Y.numel() != T * self.out_features:
             raise TypeError(f"Y must be a contiguous fp16 CUDA tensor [tokens][{self.out_features}]")
         if X.get_device() != Y.get_device() or X.get_device() != self._index:
             raise ValueError(f"X on {X.device}, Y on {Y.device}, the layer on {self.device}")
         if T > self._ws_tokens or self._ws is None:
-            self._workspace(T)
+            self._workspace(T, stream)
         if stream is None:
             return T, Y, int(_raw_stream(X.get_device())) if _raw_stream is not None else _stream(None, X.device)
         return T, Y, _stream(stream, X.device)
@@ -600,7 +610,7 @@ def _launch(fn, device: int, stream, *args) -> int:
     return fn(*args, _stream(stream, torch.device("cuda", device)))
 
 
-def _norm_args(X, weight, residual, bias, H):
+def _norm_args(X, weight, residual, bias, H, stream):
     """Shape, pointers and H of a norm after the checks its two forms share; H
     is allocated when a residual, a bias or fp32 sums make it differ from X."""
     if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in (torch.float16, torch.float32):
@@ -610,7 +620,7 @@ def _norm_args(X, weight, residual, bias, H):
     x = _dev(X, X.dtype, "X")
     row = shape[1:]
     if H is None and (residual is not None or bias is not None or x32):
-        H = torch.empty(shape, dtype=torch.float16, device=X.device)
+        H = _empty(shape, torch.float16, X.device, stream)
     return shape, (x, int(x32),
                    None if residual is None else _f16(residual, shape, dev, "residual"),
                    None if bias is None else _f16(bias, row, dev, "bias"),
@@ -618,10 +628,10 @@ def _norm_args(X, weight, residual, bias, H):
         None if H is None else _f16(H, shape, dev, "H"), H
 
 
-def _out(t, shape, dtype, device, name):
+def _out(t, shape, dtype, device, name, stream):
     """An output: allocated, or the given tensor after its checks."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     _dev(t, dtype, name)
     if t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {list(shape)} on {device}, got {list(t.shape)} on {t.device}")
@@ -635,9 +645,9 @@ def paro_rmsnorm(X: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     root-mean-square norm times weight. X fp16, or fp32 sums of a row-parallel
     layer. H is None when nothing is added to an fp16 X and no H is given;
     H=residual updates the residual stream in place."""
-    shape, args, h, H = _norm_args(X, weight, residual, bias, H)
+    shape, args, h, H = _norm_args(X, weight, residual, bias, H, stream)
     if Y is None:
-        Y = torch.empty(shape, dtype=torch.float16, device=X.device)
+        Y = _empty(shape, torch.float16, X.device, stream)
     dev = X.get_device()
     st = _launch(lib().paro_rmsnorm, dev, stream, *args, eps, h, _f16(Y, shape, dev, "Y"), *shape)
     if st != PARO_OK:
@@ -651,13 +661,13 @@ def paro_rmsnorm_q8(X: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     """(codes, scales, H): paro_rmsnorm with Y as float8_e4m3fn codes and fp32
     scales [tokens][ceil(features / 128)] (scale_group 128) or [tokens][1]
     (scale_group 0: one scale per row)."""
-    shape, args, h, H = _norm_args(X, weight, residual, bias, H)
+    shape, args, h, H = _norm_args(X, weight, residual, bias, H, stream)
     T, F = shape
     scales, dev = (T, -(-F // 128) if scale_group else 1), X.get_device()
     if Y is None:
-        Y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=X.device)
+        Y = _empty(shape, torch.float8_e4m3fn, X.device, stream)
     if S is None:
-        S = torch.empty(scales, dtype=torch.float32, device=X.device)
+        S = _empty(scales, torch.float32, X.device, stream)
     st = _launch(lib().paro_rmsnorm_q8, dev, stream, *args, eps, scale_group, h,
                  _f16(Y, shape, dev, "Y", torch.float8_e4m3fn), _f16(S, scales, dev, "S", torch.float32), T, F)
     if st != PARO_OK:
@@ -672,7 +682,7 @@ def paro_q8_expand(Q: torch.Tensor, S: torch.Tensor, scale_group: int = 128, Y: 
     if Q.dim() != 2 or S.shape != (Q.shape[0], -(-Q.shape[1] // 128) if scale_group else 1) or S.device != Q.device:
         raise ValueError("S must hold one scale per row, or per 128 channels of a row, of Q [tokens][features]")
     T, F = Q.shape
-    Y = _out(Y, (T, F), torch.float16, Q.device, "Y")
+    Y = _out(Y, (T, F), torch.float16, Q.device, "Y", stream)
     with _on(Q.device):
         _check("paro_q8_expand", lib().paro_q8_expand(q, s, scale_group, Y.data_ptr(), T, F,
                                                       _stream(stream, Q.device)))

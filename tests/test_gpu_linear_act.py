@@ -389,6 +389,41 @@ def test_side_stream_calls_without_a_workspace(B):
     assert all(torch.equal(y, want_y) for y in ys) and all(torch.equal(h, want_h) for h in hs)
 
 
+def test_side_stream_outputs_do_not_take_memory_still_in_use(B):
+    """Tensors freed while the current stream still has work on them do not
+    become the outputs or the workspace of a call on another stream."""
+    T, in_f, out_f = 300, 1024, 512
+    L = Layer(B, T, in_f, out_f, seed=8)
+    G = B.paro_pack_gated(L.q, L.s, L.z)
+    w = torch.ones(in_f, dtype=torch.float16, device="cuda")
+    layer = B.ParoLinear(L.rot, *L.packed, in_f, out_f, act="silu")
+    calls = {
+        "act": (lambda st: B.paro_linear_act(L.rot, L.x, *L.packed, out_f, stream=st), (2 * T * out_f,)),
+        "gated": (lambda st: B.paro_linear_gated(L.rot, L.x, *G, out_f // 2, stream=st), (T * out_f,)),
+        "norm": (lambda st: B.paro_rmsnorm(L.x, w, 1e-6, residual=L.x, stream=st), (2 * T * in_f,) * 2),
+        "q8": (lambda st: B.paro_rmsnorm_q8(L.x, w, 1e-6, residual=L.x, stream=st), (T * in_f, 2 * T * in_f, 4 * T * in_f // 128)),
+        "layer": (lambda st: layer(L.x, stream=st), (2 * T * out_f,)),
+    }
+    st = torch.cuda.Stream()
+    ws = B.paro_linear_workspace_size(T, in_f, out_f)
+    for name, (call, sizes) in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        for stream in (st, st.cuda_stream):
+            held = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in (*sizes, ws)]
+            torch.cuda._sleep(20_000_000)                   # about 10 ms: the copies below come after the call
+            copies = [h.clone() for h in held]
+            del held
+            got = call(stream)
+            torch.cuda.synchronize()
+            assert all(bool((c == 77).all()) for c in copies), name
+            for g, e in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+                assert torch.equal(g.view(torch.uint8), e.view(torch.uint8)), name
+    y = B.paro_linear_act(L.rot, L.x, *L.packed, out_f, stream=0)       # the default stream by its raw handle
+    torch.cuda.synchronize()
+    assert torch.equal(y, calls["act"][0](None))
+
+
 def test_a_captured_call_survives_a_larger_batch(B):
     """A graph goes on using the workspace it was captured with after the
     prepared layer has grown another."""
