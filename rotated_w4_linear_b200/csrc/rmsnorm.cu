@@ -71,6 +71,22 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// The scale of channels whose largest |v w| is m, and k = rms / scale: one
+// product per channel instead of y and y / s. The approximate reciprocal is
+// off by 2^-22, the codes' own rounding by up to 2^-4. k is held finite, for
+// the zeros of an all-zero row with a tiny eps; a NaN stays one.
+__device__ __forceinline__ float q8_scale(float m, float rms, float& k) {
+    const float s = fmaxf(m * rms * (1.f / kE4m3Max), kScaleFloor);
+    k = __fdividef(rms, s);
+    k = k > 3.402823466e38f ? 3.402823466e38f : k;
+    return s;
+}
+// The warp's largest of values without a sign: their bits compare as integers
+// do (a NaN comes out on top; its row's scale is then the floor).
+__device__ __forceinline__ float warp_max(float v) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
 }  // namespace
 
 enum : int { kNormF16 = 0, kNormQ8Group = 1, kNormQ8Row = 2 };
@@ -117,6 +133,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, 
                                          float (&v)[VPT][8], const uint4 (&r)[VPT], NormWeights<VPT>& w,
                                          float2* part) {
     float ss = 0.f, mx = 0.f;
+    float gm[VPT];                                         // largest |v w| of the vector's 128 channels
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = p.t0 + j * p.tr;
@@ -135,14 +152,22 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, 
         for (int e = 0; e < 8; ++e) {
             ss = fmaf(v[j][e], v[j][e], ss);
             v[j][e] *= f[e];                               // v w from here on
-            if (OUT == kNormQ8Row) mx = fmaxf(mx, fabsf(v[j][e]));
         }
+        if (OUT != kNormF16) {
+            gm[j] = fabsf(v[j][0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) gm[j] = fmaxf(gm[j], fabsf(v[j][e]));
+            mx = fmaxf(mx, gm[j]);
+        }
+        if (OUT == kNormQ8Group)                           // lanes 0-15 and 16-31 are one group each
+#pragma unroll
+            for (int o = 8; o; o >>= 1) gm[j] = fmaxf(gm[j], __shfl_xor_sync(0xffffffffu, gm[j], o));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (OUT == kNormQ8Row) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
+    if (OUT == kNormQ8Row) mx = warp_max(mx);
     if (a.wpr > 1) {
         if (p.lane == 0) part[p.warp] = make_float2(ss, mx);
         __syncthreads();
@@ -152,42 +177,32 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, 
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (OUT == kNormQ8Row) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         }
+        if (OUT == kNormQ8Row) mx = warp_max(mx);
     }
     const float rms = rsqrtf(ss * a.inv_f + a.eps);        // 2 ulp; infinity gives 0
-    float inv_row = 0.f;
+    float k = rms;                                         // v w k: the norm, or the norm over its scale
     if (OUT == kNormQ8Row) {
-        const float s = fmaxf(mx * rms / kE4m3Max, kScaleFloor);
-        inv_row = 1.f / s;
+        const float s = q8_scale(mx, rms, k);
         if (live && p.wr == 0 && p.lane == 0) a.S[row] = s;
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = p.t0 + j * p.tr;
         const bool in = live && i < a.nvec;
+        if (OUT == kNormQ8Group) {
+            const float s = q8_scale(gm[j], rms, k);
+            if (in && (p.lane & 15) == 0) a.S[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s;
+        }
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = v[j][e] * rms;
-        if (OUT == kNormF16) {
-            if (in) static_cast<uint4*>(a.Y)[row * a.nvec + i] = pack8(y);
-        } else {
-            float inv = inv_row;
-            if (OUT == kNormQ8Group) {                     // lanes 0-15 and 16-31 are one group each
-                float m = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-#pragma unroll
-                for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float s = fmaxf(m / kE4m3Max, kScaleFloor);
-                inv = 1.f / s;
-                if (in && (p.lane & 15) == 0) a.S[row * ((a.nvec + 15) >> 4) + (i >> 4)] = s;
-            }
-            if (in)
-                static_cast<uint2*>(a.Y)[row * a.nvec + i] =
-                    make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                               pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-        }
+        for (int e = 0; e < 8; ++e) y[e] = v[j][e] * k;
+        if (!in) continue;
+        if (OUT == kNormF16)
+            static_cast<uint4*>(a.Y)[row * a.nvec + i] = pack8(y);
+        else
+            static_cast<uint2*>(a.Y)[row * a.nvec + i] =
+                make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
     }
 }
 
