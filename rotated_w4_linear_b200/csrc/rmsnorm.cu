@@ -17,13 +17,15 @@
 // row's scale: max|y| = max|v w| / rms exactly, since one rounded product is
 // monotonic) share one cross-warp reduction in a fixed order, so a row's
 // result does not depend on the batch. A 128-channel group is sixteen
-// neighbouring lanes, so its scale is a four-step shuffle.
+// neighbouring lanes, so its largest |v w| is a four-step shuffle, done before
+// the row's barrier too.
 // Measured (fp16 x, residual and H; HBM copy peak 6552 GB/s): 8192 x 4096
-// 42.0 us, 6390 GB/s; 4096 x 5120 with codes 26.6 us (128 channels per scale)
-// and 29.3 us (one scale per row), 5520 and 5000 GB/s; 2048 x 8192 from fp32
-// 27.1 us, 6190 GB/s; one token of 4096 1.5 us, which is launch and latency. A persistent form with a
-// three-deep cp.async ring of rows ran slower (50.2 and 30.0 us): enough CTAs
-// are resident that one's loads cover another's reduction.
+// 42.0-43.0 us, 6250-6390 GB/s; 4096 x 5120 with codes 25.9 us (128 channels
+// per scale) and 28.0 us (one scale per row), 5660 and 5250 GB/s; 2048 x 8192
+// from fp32 27.1 us, 6190 GB/s; one token of 4096 1.5 us, which is launch and
+// latency. A persistent form with a three-deep cp.async ring of rows ran
+// slower (50.2 and 30.0 us): enough CTAs are resident that one's loads cover
+// another's reduction.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -71,14 +73,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// The scale of channels whose largest |v w| is m, and k = rms / scale: one
-// product per channel instead of y and y / s. The approximate reciprocal is
-// off by 2^-22, the codes' own rounding by up to 2^-4. k is held finite, for
-// the zeros of an all-zero row with a tiny eps; a NaN stays one.
+// The scale of channels whose largest |v w| is m, and k = rms / scale, so that
+// a code takes one product: e4m3(v w k). The approximate quotient is off by
+// 2^-22, the codes' own rounding by up to 2^-4.
 __device__ __forceinline__ float q8_scale(float m, float rms, float& k) {
     const float s = fmaxf(m * rms * (1.f / kE4m3Max), kScaleFloor);
     k = __fdividef(rms, s);
-    k = k > 3.402823466e38f ? 3.402823466e38f : k;
     return s;
 }
 // The warp's largest of values without a sign: their bits compare as integers
@@ -180,7 +180,17 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormPlace& p, 
         }
         if (OUT == kNormQ8Row) mx = warp_max(mx);
     }
-    const float rms = rsqrtf(ss * a.inv_f + a.eps);        // 2 ulp; infinity gives 0
+    float rms = rsqrtf(ss * a.inv_f + a.eps);        // 2 ulp; infinity gives 0
+    if (OUT != kNormF16 && rms > 1.34217728e8f) {          // 2^27: k could overflow, so v w takes rms at once
+        mx *= rms;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            gm[j] *= rms;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] *= rms;
+        }
+        rms = 1.f;
+    }
     float k = rms;                                         // v w k: the norm, or the norm over its scale
     if (OUT == kNormQ8Row) {
         const float s = q8_scale(mx, rms, k);
@@ -223,11 +233,11 @@ __device__ __forceinline__ void unpack_x(const uint4 (&x)[X32 ? 2 : 1], float v[
 
 }  // namespace
 
-// Registers per thread are held to what keeps as many warps resident as the
-// loads need (two vectors per thread: 48 registers, 4096 x 5120 with codes
-// 26.6 us; 56 took 34.8 us, 40 took 32.1 us).
-template <int VPT, bool X32, int OUT>
-__global__ void __maxnreg__(VPT == 2 ? 48 : VPT == 1 ? 32 : 64) rmsnorm_kernel(const NormArgs a) {
+// REGS, registers per thread, are held to what keeps as many warps resident
+// as the loads need: an SM quarter holds 16 warps at 32, 12 at 40, 10 at 48,
+// 8 at 64 and 7 at 72 (see launch_rmsnorm).
+template <int VPT, bool X32, int OUT, int REGS>
+__global__ void __maxnreg__(REGS) rmsnorm_kernel(const NormArgs a) {
     // the next kernel may launch; it reads nothing of ours before this grid is complete
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr int XV = X32 ? 2 : 1;
@@ -298,24 +308,20 @@ cudaLaunchConfig_t pdl_config(unsigned grid, unsigned block, cudaStream_t s, cud
     return cfg;
 }
 
-template <int VPT, bool X32, int OUT>
+template <int VPT, bool X32, int OUT, int REGS>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg =
         pdl_config((unsigned)((a.T + a.rows - 1) / a.rows), (unsigned)(32 * a.wpr * a.rows), s, &attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rmsnorm_kernel<VPT, X32, OUT>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rmsnorm_kernel<VPT, X32, OUT, REGS>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int VPT>
-cudaError_t launch_norm_v(const NormArgs& a, bool x32, int out, cudaStream_t s) {
-    if (x32)
-        return out == kNormF16 ? launch_norm<VPT, true, kNormF16>(a, s)
-               : out == kNormQ8Group ? launch_norm<VPT, true, kNormQ8Group>(a, s)
-                                     : launch_norm<VPT, true, kNormQ8Row>(a, s);
-    return out == kNormF16 ? launch_norm<VPT, false, kNormF16>(a, s)
-           : out == kNormQ8Group ? launch_norm<VPT, false, kNormQ8Group>(a, s)
-                                 : launch_norm<VPT, false, kNormQ8Row>(a, s);
+template <int VPT, bool X32, int REGS>
+cudaError_t launch_norm_out(const NormArgs& a, int out, cudaStream_t s) {
+    return out == kNormF16       ? launch_norm<VPT, X32, kNormF16, REGS>(a, s)
+           : out == kNormQ8Group ? launch_norm<VPT, X32, kNormQ8Group, REGS>(a, s)
+                                 : launch_norm<VPT, X32, kNormQ8Row, REGS>(a, s);
 }
 
 }  // namespace
@@ -336,19 +342,34 @@ cudaError_t launch_rmsnorm(const void* x, bool x_fp32, const void* r, const void
     a.inv_f = (float)(1.0 / (double)F);
     a.eps = eps;
     const int out = !S ? kNormF16 : scale_group ? kNormQ8Group : kNormQ8Row;
-    // The split of a row over threads goes by its width alone, so a row's
-    // sums have the same order in every batch: one vector per thread up to 11
-    // warps, then two, then four where 1024 threads would not do (8192 x 4096:
-    // 42.0 us with two, 43.0 with one; 4096 x 5120 with codes 26.6 with two,
-    // 30.0 with one, 31.4 with four; 8192 x 2560 from fp32 32.8 with one, 34.1
-    // with two).
+    // The split of a row over threads goes by its width (and the type of x)
+    // alone, so a row's sums have the same order in every batch: one vector
+    // per thread up to 11 warps, then two, then four where two would leave
+    // one CTA on an SM (above 20 warps at 48 registers). Measured: 8192 x 4096
+    // 42.0 us with two, 43.0 with one; 8192 x 2560 from fp32 32.8 with one,
+    // 34.1 with two; 2034 x 12288 34.1 with four, 40.9 with two, and with a
+    // scale per row 35.5 against 44.4; from fp32 42.3 against 44.4. Four
+    // vectors of fp32 take 72 registers (with 64, which spill, 45.7), which leave
+    // one CTA above 14 warps: there two vectors again while they fit (1525 x
+    // 16384 from fp32 43.0, with four 49.1).
     const int nw = (a.nvec + 31) / 32;                      // warps at one vector per thread
-    const int vpt = nw > 64 ? 4 : nw > 11 ? 2 : 1;
+    const int vpt = nw <= 11 ? 1 : nw <= 40 || (x_fp32 && nw > 56 && nw <= 64) ? 2 : 4;
     a.wpr = (nw + vpt - 1) / vpt;
     a.rows = T > 296 && a.wpr < 8 ? 8 / a.wpr : 1;
-    return vpt == 4 ? launch_norm_v<4>(a, x_fp32, out, s)
-           : vpt == 2 ? launch_norm_v<2>(a, x_fp32, out, s)
-                      : launch_norm_v<1>(a, x_fp32, out, s);
+    if (x_fp32) {
+        if (vpt == 1) return launch_norm_out<1, true, 32>(a, out, s);
+        if (vpt == 2) return launch_norm_out<2, true, 48>(a, out, s);
+        return a.wpr <= 28 ? launch_norm_out<4, true, 72>(a, out, s)
+                           : launch_norm_out<4, true, 64>(a, out, s);   // 32 warps fit
+    }
+    if (vpt == 1) return launch_norm_out<1, false, 32>(a, out, s);
+    if (vpt == 4) return launch_norm_out<4, false, 64>(a, out, s);
+    // A scale per row has the longest way from its loads to its stores: where
+    // 40 registers (4 bytes spilled) let one more CTA in than 48, it gains
+    // (3051 x 8192 32.0 us against 36.2; where they do not, 5120 wide, 33.4
+    // against 32.8). The other outputs do not: 6144 wide 33.4 against 32.1.
+    if (out == kNormQ8Row && 48 / a.wpr > 40 / a.wpr) return launch_norm<2, false, kNormQ8Row, 40>(a, s);
+    return launch_norm_out<2, false, 48>(a, out, s);
 }
 
 cudaError_t launch_q8_expand(const void* Q, const float* S, int scale_group, void* Y, int64_t T, int64_t F,

@@ -85,7 +85,8 @@ def check_q8(Q, S, y, ey, group):
 
 
 SHAPES = [(1, 16), (3, 48), (2, 128), (5, 144), (1, 4096), (16, 4096), (17, 2560), (300, 272), (301, 1040),
-          (1023, 2576), (7, 8192), (5, 8208), (3, 16384), (2, 16400), (3, 17408), (2, 32768)]
+          (1023, 2576), (7, 8192), (5, 8208), (3, 10768), (2, 14336), (3, 14352),
+          (3, 16384), (2, 16400), (3, 17408), (2, 28688), (2, 32768)]
 
 
 @pytest.mark.parametrize("T,F", SHAPES)
@@ -176,6 +177,27 @@ def test_small_values_and_a_large_eps(B):
         check_y(B.paro_rmsnorm(dev(x), dev(w), eps)[0], y, ey)
         Q, S, _ = B.paro_rmsnorm_q8(dev(x), dev(w), eps)
         check_q8(Q, S, y, ey, 128)
+
+
+def test_channels_below_the_scale_floor(B):
+    """Zeros, and values whose scale is the floor, under an eps so small that
+    the norm's factor over the scale exceeds fp32."""
+    T, F, eps = 3, 256, 2.0 ** -60
+    rng = np.random.default_rng(4)
+    x = np.zeros((T, F), np.float32)
+    x[1, :128] = rng.standard_normal(128).astype(np.float32) * 1e-15     # the row's second group is zero
+    x[2] = rng.standard_normal(F).astype(np.float32) * np.float32(2.0 ** -123)    # y about 2^-93: codes above the floor
+    x[2, :128] *= np.float32(2.0 ** -5)                     # and below it
+    w = np.full(F, 1.5, np.float16)
+    ey = 2.0 ** -18
+    _, y = O.rmsnorm(x, w, eps)
+    for group in (128, 0):
+        Q, S, _ = B.paro_rmsnorm_q8(dev(x), dev(w), eps, scale_group=group)
+        q, s = host(Q), host(S)
+        assert np.all(q[0] == 0) and np.all(q[1, 128:] == 0) and np.all(np.isfinite(q)) and np.all(s >= 2.0 ** -100)
+        check_q8(Q[:2], S[:2], y[:2], ey * np.abs(y[:2]), group)
+        each = s[2, np.arange(F) // (128 if group else F)]
+        assert np.all(np.abs(q[2] * each - y[2]) <= 2.0 ** -4 * np.abs(y[2]) + 2.0 ** -10 * each + ey * np.abs(y[2]))
 
 
 def test_on_a_side_stream_and_in_a_graph(B):
