@@ -17,13 +17,14 @@
 //   warps 0, 19 (20)  TMA producers: per stage of 128 channels the CTA's half of
 //               the tokens of X' (two 64-channel boxes, 128-byte swizzle), and
 //               the int4 codes of its 8 row blocks with their scales and zeros,
-//               whose ring is deeper;
+//               whose ring is deeper; both CTAs' loads of X' complete on the
+//               leader's barrier of the stage;
 //   warps 3-10 (BN < 256: 3-14)  dequantise (w_hat = fp16((q - z) s), as the
 //               other kernels do) into a ring of tensor-memory stages: two
 //               (three) groups of four warps take turns, a warp takes one
 //               quarter of the rows of its group's stage;
-//   warp 2      gate: one lane reports to the pair's leader when its CTA's X'
-//               and w_hat of a stage are there;
+//   warp 2      gate: one lane reports to the pair's leader when its CTA's w_hat
+//               of a stage, and in the leader X', is there;
 //   warp 1      tensor memory; in the leader the warp issues the MMAs (A from
 //               tensor memory, B from shared memory) of a stage that both
 //               gates have reported, and commits it back to both CTAs;
@@ -133,29 +134,30 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive at a barrier of the cluster's other CTA, and wait for such arrivals.
-// Relaxed: what they order is tensor memory (written with tcgen05.st, read by
-// the MMA), which goes by the tcgen05 fences on both sides, and shared memory
-// that TMA wrote and the MMA reads; no ordinary loads and stores meet here. A
-// release at cluster scope costs about 900 cycles.
+// Arrive at a barrier of the cluster's other CTA. Relaxed: what it orders is
+// tensor memory alone (written with tcgen05.st, read by the MMA), which goes by
+// the tcgen05 fences on both sides. A release at cluster scope costs about 900
+// cycles.
 __device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_other(uint32_t bar, uint32_t parity) {
+// Wait for arrivals and loads of both CTAs: what either CTA's TMA wrote before
+// it completed on this barrier is visible to what the warp does next.
+__device__ __forceinline__ bool mbar_try_wait_pair(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_other(uint32_t bar, uint32_t parity, unsigned int fault,
-                                                volatile uint32_t* abort) {
-    if (mbar_try_wait_other(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, unsigned int fault,
+                                               volatile uint32_t* abort) {
+    if (mbar_try_wait_pair(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_other(bar, parity)) return true;
+        if (mbar_try_wait_pair(bar, parity)) return true;
         if ((it & 255u) == 0) {
             if (*abort) return false;
             if (global_ns() - t0 > kWaitLimitNs) {
@@ -165,6 +167,13 @@ __device__ __forceinline__ bool mbar_wait_other(uint32_t bar, uint32_t parity, u
             }
         }
     }
+}
+// 2-D TMA tile load into this CTA's shared memory whose bytes complete on a
+// barrier of either CTA of the pair (`bar` is a cluster address). No multicast.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {   // one warp of each CTA
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
@@ -358,7 +367,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXStages; ++s) {
-            mbar_init(xfull0 + 8 * s, 1);
+            mbar_init(xfull0 + 8 * s, 1);                 // leader: both CTAs' halves of X' (the other CTA's is not used)
             mbar_init(free0 + 8 * s, 1);                  // the MMAs on X' stage and w_hat stage s are done
             mbar_init(afull0 + 8 * s, 4);                 // the dequantisation warps of one group
             mbar_init(go0 + 8 * s, 2);                    // leader: both CTAs' gates
@@ -408,6 +417,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         RingPos<kWStages> pw;
         if (w0) pw.next();
         uint32_t mine = 0;                                // loads issued by this warp
+        const uint32_t xfull_leader0 = map_to_rank(xfull0, crank & ~1u);
         int ahead = w0;                                   // stages to the warp's next one, over tile borders
         bool ok = true;
         for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
@@ -421,11 +431,15 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (xs) {
-                    const uint32_t bar = xfull0 + 8 * slot, dst = sX + slot * kXStage;
+                    // The leader expects the bytes of both CTAs. The other CTA's
+                    // may come first: the phase stays open until the leader's
+                    // arrival, and the slot's next loads wait for the MMAs of
+                    // these (free), so no bytes count in a later phase.
+                    const uint32_t bar = xfull_leader0 + 8 * slot, dst = sX + slot * kXStage;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, (uint32_t)bn * 128);
-                        tma_load_2d(dst, &tm_x, kb * 128, n0, bar);
-                        tma_load_2d(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
+                        if (rank == 0) mbar_arrive_expect_tx(xfull0 + 8 * slot, 2 * (uint32_t)bn * 128);
+                        tma_load_2d_pair(dst, &tm_x, kb * 128, n0, bar);
+                        tma_load_2d_pair(dst + kHalfX, &tm_x, kb * 128 + 64, n0, bar);
                     }
                     px.next();
                 } else {
@@ -447,19 +461,29 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             ahead = i - nk;
         }
         if (*abort) {   // drain: every issued load must land before the CTA exits
-            // the j-th load of this warp went to slot (w0 + step j) mod N
-            const int n = xs ? kXStages : kWStages, per = n / step;
-            for (int t = 0; t < per; ++t) {
-                const uint32_t uses = (mine + (uint32_t)(per - 1 - t)) / (uint32_t)per;   // of its t-th slot
-                if (uses > 0)
-                    mbar_wait((xs ? xfull0 : wfull0) + 8 * (w0 + step * t), (uses - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
+            if (xs) {
+                // the barrier that counts this CTA's X' also counts the other
+                // CTA's, which may have stopped short: wait out the limit, far
+                // longer than a load takes
+                const uint64_t t0 = global_ns();
+                while (mine > 0 && global_ns() - t0 <= kWaitLimitNs) __nanosleep(100000);
+            } else {
+                // the j-th load of this warp went to slot (w0 + step j) mod N
+                const int per = kWStages / step;
+                for (int t = 0; t < per; ++t) {
+                    const uint32_t uses = (mine + (uint32_t)(per - 1 - t)) / (uint32_t)per;   // of its t-th slot
+                    if (uses > 0)
+                        mbar_wait(wfull0 + 8 * (w0 + step * t), (uses - 1) & 1, kFaultGemmPair + kFaultDrainWait, nullptr);
+                }
             }
         }
     } else if (warp == 2) {
         if (lane == 0) {
             // ---- gate: one report per stage and CTA to the leader's MMA warp,
             // which then looks at one barrier instead of three (a look takes
-            // about 100 cycles)
+            // about 100 cycles): the other CTA's that its w_hat is there, the
+            // leader's that its own w_hat and both halves of X' are (4096 ->
+            // 28672 at 64 tokens 36.7 us; with the MMA warp looking at X' too 38.3)
             const uint32_t go_leader0 = map_to_rank(go0, crank & ~1u);
             RingPos<kXStages> p;
             uint32_t tiles = 0;
@@ -468,12 +492,13 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 // the sums of the tile before are out of this CTA's tensor memory
                 if (tiles > 0) ok = mbar_wait(accfree, (tiles - 1) & 1, kFaultGemmPair + kFaultMmaWait, abort);
                 for (int i = 0; ok && i < nk; ++i, p.next()) {
-                    ok = mbar_wait(xfull0 + 8 * p.slot, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort) &&
+                    ok = (rank != 0 || mbar_wait_pair(xfull0 + 8 * p.slot, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort)) &&
                          mbar_wait(afull0 + 8 * p.slot, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort);
                     if (!ok) break;
                     tc_fence_after();
                     tc_fence_before();
-                    mbar_arrive_other(go_leader0 + 8 * p.slot);
+                    if (rank == 0) mbar_arrive(go0 + 8 * p.slot);      // release: X' goes with it
+                    else mbar_arrive_other(go_leader0 + 8 * p.slot);
                 }
             }
         }
@@ -489,7 +514,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             for (int tile = first_tile; ok && tile < a.ntiles; tile += nclusters) {
                 for (int i = 0; i < nk; ++i, p.next()) {
                     const int s = p.slot;
-                    ok = __all_sync(0xffffffffu, mbar_wait_other(go0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort));
+                    ok = __all_sync(0xffffffffu, mbar_wait_pair(go0 + 8 * s, p.use & 1, kFaultGemmPair + kFaultMmaWait, abort));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t b = umma_desc_sw128_kmajor(sX + s * kXStage);
