@@ -93,11 +93,13 @@ struct PairCfg {
     static constexpr uint32_t kSums = kSplit ? BN * 128 * 4 : 0;       // in the rings' space
     static constexpr uint32_t kBody = kRings > kSums ? kRings : kSums;
     static constexpr int kBars = 4 * kXStages + 2 * kWStages + 3 + 16;
-    // Never less than 160 KB: the kernel takes all of an SM's tensor memory, so
+    // Never less than 200 KB: the kernel takes all of an SM's tensor memory, so
     // a second kernel that wants some must not share the SM with it (two that
     // each held one SM of a pair would wait for each other)
     static constexpr size_t kUsed = 1024 + (size_t)kBody + 8 * kBars + 16;
-    static constexpr size_t kSmem = kUsed > 160 * 1024 ? kUsed : 160 * 1024;
+    static constexpr size_t kSmem = kUsed > 200 * 1024 ? kUsed : 200 * 1024;
+    static_assert(kSmem + kLeastTmemSmem + 2 * kCtaReservedBytes > kSmSharedBytes,
+                  "a second kernel with tensor memory would fit on the SM");
     static_assert(BN + 64 * kXStages <= 512, "tensor memory");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -334,9 +336,6 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_z,
                  const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
                  const PairArgs a) {
-    // the next kernel's CTAs may take SMs as this grid's leave them; it reads
-    // nothing of ours before this grid is complete
-    asm volatile("griddepcontrol.launch_dependents;");
     using C = PairCfg<BN>;
     constexpr int kXStages = C::kXStages, kWStages = C::kWStages;
     constexpr uint32_t kHalfX = C::kHalfX, kXStage = C::kXStage;
@@ -392,6 +391,11 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     if (warp == 1) tmem_alloc_pair(smem_addr(tslot), 512);
     tc_fence_before();
     __syncthreads();
+    // The next kernel's CTAs may take SMs as this grid's leave them; it reads
+    // nothing of ours before this grid is complete. Not before every CTA has its
+    // tensor memory: a dependent that took some of an SM's first would wait for
+    // this grid, and this grid for it.
+    asm volatile("griddepcontrol.launch_dependents;");
     cluster_arrive_wait();                                // the other CTA's barriers exist too
     tc_fence_after();
     const uint32_t tbase = *tslot;

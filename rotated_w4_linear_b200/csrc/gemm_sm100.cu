@@ -333,6 +333,7 @@ template <int BN, int STAGES, int DQG, int NACC>
 cudaError_t launch_cfg(const CUtensorMap* tm, const GemmArgs& a, int mt, int nt, cudaStream_t s) {
     constexpr size_t smem = STAGES * (BN * 128 + kWStage + kSStage + kZStage) + (3 * STAGES + 2) * 8 +
                             16 * (128 + 4) * 4 + 1024;
+    static_assert(smem >= kLeastTmemSmem, "a kernel that takes all of an SM's tensor memory counts on it");
     // kernel attributes, set once per device (double-checked under a lock)
     static std::atomic<bool> configured[64] = {};
     static std::mutex mu;

@@ -37,6 +37,13 @@ constexpr size_t kRotMatBytes = 4 * 128 * 128;
 // lo fp16 of 256 (k) x 128 (n).
 constexpr size_t kRotMat256Bytes = 4 * 256 * 128;
 
+// Shared memory of an SM (1 KB of it is reserved for each resident CTA), and
+// the least that a kernel of this library which allocates tensor memory asks
+// for (the single-CTA GEMM with 64 tokens per tile; each of them checks it). A
+// kernel that takes a whole SM's tensor memory asks for so much that none of
+// them fits beside it.
+constexpr size_t kSmSharedBytes = 228 * 1024, kCtaReservedBytes = 1024, kLeastTmemSmem = 58 * 1024;
+
 // 2-D TMA descriptor of a row-major tensor [outer][inner] (driver entry point).
 bool encode_tma_2d(CUtensorMap* tm, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);

@@ -487,6 +487,8 @@ cudaError_t launch_rotate_tc(const RotDev& r, const void* X, void* Xr, int64_t T
     constexpr int S = kTcStages, S256 = 3;
     constexpr size_t smem = tc_smem<S>();
     constexpr size_t smem256 = 8 * kHalfTile + S256 * kXStage + (2 * S256 + 12) * 8 + 1024;
+    static_assert(smem >= kLeastTmemSmem && smem256 >= kLeastTmemSmem,
+                  "a kernel that takes all of an SM's tensor memory counts on it");
     static std::atomic<bool> configured[64] = {}, configured256[64] = {};
     static std::mutex mu;
     int dev = 0;

@@ -1,5 +1,5 @@
 """The contraction on CTA pairs (paro_linear_act and paro_linear_gated above 16
-tokens): what its two CTAs exchange."""
+tokens): what its two CTAs exchange, and what shares an SM with it."""
 import pytest
 import torch
 
@@ -47,3 +47,30 @@ def test_each_call_multiplies_its_own_tokens(B, T, n_in, n_out):
         B.paro_linear_act(None, inputs[i], *L.packed, n_out, act="silu", bias=L.bias, residual=L.residual, Y=y, ws=ws)
         B.paro_linear_gated(None, inputs[i], *G, n_out // 2, bias=L.bias, H=h, ws=ws)
         assert torch.equal(y, want[i][0]) and torch.equal(h, want[i][1]), k
+
+
+@pytest.mark.parametrize("T", [17, 40, 64])
+def test_layers_with_tensor_memory_one_after_another(B, T):
+    """Launches in a row that each allocate tensor memory, the second one before
+    the first is done (programmatic dependents): the pair kernel and the
+    single-CTA kernel's smallest form, unrotated, on one stream and on two."""
+    n_in, n_out = 1024, 37888                               # 148 row tiles of 256: two rounds of pairs
+    L = Layer(B, T, n_in, n_out, rotated=False, bias=False, seed=T)
+    want, bound = R.linear_act(L.x, L.w, "none")
+    one = B.paro_linear_act(None, L.x, *L.packed, n_out)
+    two = B.paro_linear_ex(None, L.x, *L.packed, n_out)
+    close(one, want, bound)
+    close(two, want, bound)
+    ys = [torch.empty_like(one) for _ in range(4)]
+    side = torch.cuda.Stream()
+    ws = [B.workspace(T, n_in, n_out) for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(100):
+        B.paro_linear_act(None, L.x, *L.packed, n_out, Y=ys[0], ws=ws[0])
+        B.paro_linear_ex(None, L.x, *L.packed, n_out, Y=ys[1], ws=ws[0])
+        if k >= 50:
+            B.paro_linear_ex(None, L.x, *L.packed, n_out, Y=ys[2], ws=ws[1], stream=side)
+            B.paro_linear_act(None, L.x, *L.packed, n_out, Y=ys[3], ws=ws[1], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], one) and torch.equal(ys[3], one)
+    assert torch.equal(ys[1], two) and torch.equal(ys[2], two)
