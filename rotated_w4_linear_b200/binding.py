@@ -121,6 +121,19 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.data_ptr()
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream` (None: the current one),
+    allocated as that stream's memory: one of the current stream's could still
+    be in use there by a tensor freed before, and could be handed out there
+    again before the call has passed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Rotation:
     """Owner of a paro_rot handle (device-resident prepared rotation)."""
 
@@ -155,9 +168,10 @@ def paro_rot_create(pairs, theta, alpha, group: int = 128) -> Rotation:
 
 
 def paro_rotate(rot: Rotation, X: torch.Tensor, Xr: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    _dev(X, torch.float16, "X")
     if Xr is None:
-        Xr = torch.empty_like(X)
-    _dev(X, torch.float16, "X"), _dev(Xr, torch.float16, "Xr")
+        Xr = _empty(X.shape, torch.float16, X.device, stream)
+    _dev(Xr, torch.float16, "Xr")
     if X.shape != Xr.shape or X.dim() != 2 or X.shape[1] != rot.in_features:
         raise ValueError("X/Xr must be [tokens][in_features]")
     _check("paro_rotate", lib().paro_rotate(rot.handle, X.data_ptr(), Xr.data_ptr(), X.shape[0], _stream(stream, X.device)))
@@ -203,9 +217,7 @@ def paro_pack_weights(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=
     out_f, in_f = q.shape
     qb, sb, zb = paro_pack_size(in_f, out_f, group)
     dev = device or (q.device if q.is_cuda else torch.device("cuda", torch.cuda.current_device()))
-    qw = torch.empty(qb, dtype=torch.uint8, device=dev)
-    sp = torch.empty(sb, dtype=torch.uint8, device=dev)
-    zp = torch.empty(zb, dtype=torch.uint8, device=dev)
+    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in (qb, sb, zb))
     _check("paro_pack_weights_ex", lib().paro_pack_weights_ex(
         _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z"), in_f, out_f, group,
         qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
@@ -213,10 +225,10 @@ def paro_pack_weights(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=
 
 
 def paro_dequant(qw, sp, zp, in_features: int, out_features: int, stream=None, group: int = 128) -> torch.Tensor:
-    W = torch.empty((out_features, in_features), dtype=torch.float16, device=qw.device)
-    _check("paro_dequant_ex", lib().paro_dequant_ex(_dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"),
-                                                    _dev(zp, torch.uint8, "zeros"), in_features, out_features, group,
-                                                    W.data_ptr(), _stream(stream)))
+    pq, ps, pz = _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros")
+    W = _empty((out_features, in_features), torch.float16, qw.device, stream)
+    _check("paro_dequant_ex", lib().paro_dequant_ex(pq, ps, pz, in_features, out_features, group, W.data_ptr(),
+                                                    _stream(stream, qw.device)))
     return W
 
 
@@ -225,11 +237,12 @@ def paro_quantize_weights(rot: Rotation, W: torch.Tensor, stream=None):
     G = in / the handle's group size."""
     out_f, in_f = W.shape
     G = in_f // rot.group
-    q = torch.empty((out_f, in_f), dtype=torch.uint8, device=W.device)
-    s = torch.empty((out_f, G), dtype=torch.float16, device=W.device)
-    z = torch.empty((out_f, G), dtype=torch.uint8, device=W.device)
+    w = _dev(W, torch.float16, "W")
+    q = _empty((out_f, in_f), torch.uint8, W.device, stream)
+    s = _empty((out_f, G), torch.float16, W.device, stream)
+    z = _empty((out_f, G), torch.uint8, W.device, stream)
     _check("paro_quantize_weights", lib().paro_quantize_weights(
-        rot.handle, _dev(W, torch.float16, "W"), out_f, q.data_ptr(), s.data_ptr(), z.data_ptr(), _stream(stream)))
+        rot.handle, w, out_f, q.data_ptr(), s.data_ptr(), z.data_ptr(), _stream(stream, W.device)))
     return q, s, z
 
 
@@ -245,19 +258,6 @@ def workspace(tokens: int, in_features: int, out_features: int, device=None) -> 
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """An output or workspace of a call on `stream` (None: the current one),
-    allocated as that stream's memory: one of the current stream's could still
-    be in use there by a tensor freed before, and could be handed out there
-    again before the call has passed."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _scratch(tokens: int, in_features: int, out_features: int, device, stream) -> torch.Tensor:
     """A workspace for one call on `stream`, not filled."""
     n = paro_linear_workspace_size(tokens, in_features, out_features)
@@ -266,13 +266,14 @@ def _scratch(tokens: int, in_features: int, out_features: int, device, stream) -
 
 def paro_linear(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int,
                 Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
     if Y is None:
-        Y = torch.empty((T, out_features), dtype=torch.float16, device=X.device)
+        Y = _empty((T, out_features), torch.float16, X.device, stream)
     if ws is None:
-        ws = workspace(T, in_f, out_features, X.device)
+        ws = _scratch(T, in_f, out_features, X.device, stream)
     _check("paro_linear", lib().paro_linear(
-        rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
+        rot.handle if rot is not None else None, x,
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"),
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
@@ -283,18 +284,19 @@ def paro_linear_bias(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, bias:
                      out_features: int, Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """paro_linear + bias (fp16 [out_features] CUDA tensor, or None)."""
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
     if Y is None:
-        Y = torch.empty((T, out_features), dtype=torch.float16, device=X.device)
+        Y = _empty((T, out_features), torch.float16, X.device, stream)
     if ws is None:
-        ws = workspace(T, in_f, out_features, X.device)
+        ws = _scratch(T, in_f, out_features, X.device, stream)
     b = None
     if bias is not None:
         if bias.numel() != out_features:
             raise ValueError("bias must have out_features elements")
         b = _dev(bias, torch.float16, "bias")
     _check("paro_linear_bias", lib().paro_linear_bias(
-        rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
+        rot.handle if rot is not None else None, x,
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b,
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
@@ -308,10 +310,11 @@ def paro_rotate_once(X: torch.Tensor, pairs, theta, alpha, group: int = 128, str
     alpha = np.ascontiguousarray(alpha, dtype=np.float32)
     K = int(pairs.shape[0])
     P = int(pairs.shape[2]) if K else 0
-    Xr = torch.empty_like(X)
+    x = _dev(X, torch.float16, "X")
+    Xr = _empty(X.shape, torch.float16, X.device, stream)
     T, in_f = X.shape
     _check("paro_rotate_once", lib().paro_rotate_once(
-        _dev(X, torch.float16, "X"), _dev(Xr, torch.float16, "Xr"), T, in_f, pairs.ctypes.data if K else None,
+        x, Xr.data_ptr(), T, in_f, pairs.ctypes.data if K else None,
         theta.ctypes.data if K else None, alpha.ctypes.data, K, group, P, _stream(stream, X.device)))
     return Xr
 
@@ -325,10 +328,11 @@ def paro_linear_once(X: torch.Tensor, pairs, theta, alpha, qw, sp, zp, out_featu
     alpha = np.ascontiguousarray(alpha, dtype=np.float32)
     K = int(pairs.shape[0])
     P = int(pairs.shape[2]) if K else 0
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
-    Y = torch.empty((T, out_features), dtype=torch.float16, device=X.device)
+    Y = _empty((T, out_features), torch.float16, X.device, stream)
     _check("paro_linear_once", lib().paro_linear_once(
-        _dev(X, torch.float16, "X"), pairs.ctypes.data if K else None, theta.ctypes.data if K else None,
+        x, pairs.ctypes.data if K else None, theta.ctypes.data if K else None,
         alpha.ctypes.data, _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"),
         _dev(zp, torch.uint8, "zeros"), _dev(Y, torch.float16, "Y"), T, in_f, out_features, K, P,
         _stream(stream, X.device)))
@@ -339,18 +343,19 @@ def paro_linear_ex(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fea
                    bias: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
                    ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The layer with weights quantised in groups of `group` channels (128 or 64)."""
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
     if Y is None:
-        Y = torch.empty((T, out_features), dtype=torch.float16, device=X.device)
+        Y = _empty((T, out_features), torch.float16, X.device, stream)
     if ws is None:
-        ws = workspace(T, in_f, out_features, X.device)
+        ws = _scratch(T, in_f, out_features, X.device, stream)
     b = None
     if bias is not None:
         if bias.numel() != out_features:
             raise ValueError("bias must have out_features elements")
         b = _dev(bias, torch.float16, "bias")
     _check("paro_linear_ex", lib().paro_linear_ex(
-        rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
+        rot.handle if rot is not None else None, x,
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, group,
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
@@ -409,9 +414,7 @@ def paro_pack_gated(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=No
         raise ValueError("s and z must be [2 inter][in/group]")
     qb, sb, zb = paro_pack_size(in_f, out_f, group)
     dev = device or (q.device if q.is_cuda else torch.device("cuda", torch.cuda.current_device()))
-    qw = torch.empty(qb, dtype=torch.uint8, device=dev)
-    sp = torch.empty(sb, dtype=torch.uint8, device=dev)
-    zp = torch.empty(zb, dtype=torch.uint8, device=dev)
+    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in (qb, sb, zb))
     with _on(qw.device):
         _check("paro_pack_gated", lib().paro_pack_gated(
             _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z"), in_f, out_f // 2, group,
@@ -552,13 +555,14 @@ def paro_linear_partial(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
                         Yf: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                         stream=None) -> torch.Tensor:
     """A row-parallel rank's unrounded fp32 share of Y over its input slice."""
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
     if Yf is None:
-        Yf = torch.empty((T, out_features), dtype=torch.float32, device=X.device)
+        Yf = _empty((T, out_features), torch.float32, X.device, stream)
     if ws is None:
-        ws = workspace(T, in_f, out_features, X.device)
+        ws = _scratch(T, in_f, out_features, X.device, stream)
     _check("paro_linear_partial", lib().paro_linear_partial(
-        rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
+        rot.handle if rot is not None else None, x,
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), group,
         _dev(Yf, torch.float32, "Yf"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
@@ -568,11 +572,12 @@ def paro_linear_partial(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
 def paro_finalize(Yf: torch.Tensor, bias: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """fp16(Yf + bias), one rounding."""
+    yf = _dev(Yf, torch.float32, "Yf")
     T, out_f = Yf.shape
     if Y is None:
-        Y = torch.empty((T, out_f), dtype=torch.float16, device=Yf.device)
+        Y = _empty((T, out_f), torch.float16, Yf.device, stream)
     b = _dev(bias, torch.float16, "bias") if bias is not None else None
-    _check("paro_finalize", lib().paro_finalize(_dev(Yf, torch.float32, "Yf"), b, _dev(Y, torch.float16, "Y"), T, out_f,
+    _check("paro_finalize", lib().paro_finalize(yf, b, _dev(Y, torch.float16, "Y"), T, out_f,
                                                 _stream(stream, Yf.device)))
     return Y
 
@@ -581,11 +586,12 @@ def paro_linear_noalloc(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
                         Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Decode (tokens <= 16) with the library's static scratch: no workspace,
     no device allocation inside the call (Y is allocated here only if not given)."""
+    x = _dev(X, torch.float16, "X")
     T, in_f = X.shape
     if Y is None:
-        Y = torch.empty((T, out_features), dtype=torch.float16, device=X.device)
+        Y = _empty((T, out_features), torch.float16, X.device, stream)
     _check("paro_linear_noalloc", lib().paro_linear_noalloc(
-        rot.handle if rot is not None else None, _dev(X, torch.float16, "X"),
+        rot.handle if rot is not None else None, x,
         _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"),
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _stream(stream, X.device)))
     return Y
