@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -201,11 +202,43 @@ def paro_pack_size(in_features: int, out_features: int, group: int = 128):
     return q.value, s.value, z.value
 
 
+@functools.lru_cache(maxsize=None)
+def _packed_bytes(in_features: int, rows: int, group: int):
+    return paro_pack_size(in_features, rows, group)
+
+
+def _weights(qw, sp, zp, in_features: int, rows: int, group: int, device: int):
+    """Data pointers of packed weights, which must hold `rows` output rows of
+    in_features channels in groups of `group` and lie on CUDA device `device`:
+    the kernels read that much from there."""
+    ptrs = []
+    for name, t, need in zip(("qweight", "scales", "zeros"), (qw, sp, zp), _packed_bytes(in_features, rows, group)):
+        ptrs.append(_dev(t, torch.uint8, name))
+        if t.numel() < need:
+            raise ValueError(f"{name} holds {t.numel()} bytes, {need} needed for {rows} x {in_features} in groups of {group}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on CUDA device {device}")
+    return ptrs
+
+
 def _any(t, dtype, name) -> int:
     """Data pointer of a contiguous tensor on the device or on the host."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
     return t.data_ptr()
+
+
+def _logical(q, s, z, group: int, device: torch.device):
+    """Data pointers of logical weights for a pack into memory of `device`,
+    after checks of their sizes and that what is on a GPU is on that one."""
+    ptrs = _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z")
+    n = q.shape[0] * (q.shape[1] // group)
+    if s.numel() != n or z.numel() != n:
+        raise ValueError("s and z must be [out][in/group]")
+    for name, t in (("q", q), ("s", s), ("z", z)):
+        if t.is_cuda and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the packed weights on {device}")
+    return ptrs
 
 
 def paro_pack_weights(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=None, device=None,
@@ -215,17 +248,17 @@ def paro_pack_weights(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=
     (qweight, scales, zeros) as uint8 tensors on `device` (default: q's
     device, else the current one)."""
     out_f, in_f = q.shape
-    qb, sb, zb = paro_pack_size(in_f, out_f, group)
+    sizes = paro_pack_size(in_f, out_f, group)
     dev = device or (q.device if q.is_cuda else torch.device("cuda", torch.cuda.current_device()))
-    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in (qb, sb, zb))
+    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in sizes)
+    logical = _logical(q, s, z, group, qw.device)
     _check("paro_pack_weights_ex", lib().paro_pack_weights_ex(
-        _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z"), in_f, out_f, group,
-        qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
+        *logical, in_f, out_f, group, qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
     return qw, sp, zp
 
 
 def paro_dequant(qw, sp, zp, in_features: int, out_features: int, stream=None, group: int = 128) -> torch.Tensor:
-    pq, ps, pz = _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros")
+    pq, ps, pz = _weights(qw, sp, zp, in_features, out_features, group, qw.get_device())
     W = _empty((out_features, in_features), torch.float16, qw.device, stream)
     _check("paro_dequant_ex", lib().paro_dequant_ex(pq, ps, pz, in_features, out_features, group, W.data_ptr(),
                                                     _stream(stream, qw.device)))
@@ -274,7 +307,7 @@ def paro_linear(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_featur
         ws = _scratch(T, in_f, out_features, X.device, stream)
     _check("paro_linear", lib().paro_linear(
         rot.handle if rot is not None else None, x,
-        _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"),
+        *_weights(qw, sp, zp, in_f, out_features, 128, X.get_device()),
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
     return Y
@@ -297,7 +330,7 @@ def paro_linear_bias(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, bias:
         b = _dev(bias, torch.float16, "bias")
     _check("paro_linear_bias", lib().paro_linear_bias(
         rot.handle if rot is not None else None, x,
-        _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b,
+        *_weights(qw, sp, zp, in_f, out_features, 128, X.get_device()), b,
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
     return Y
@@ -333,8 +366,8 @@ def paro_linear_once(X: torch.Tensor, pairs, theta, alpha, qw, sp, zp, out_featu
     Y = _empty((T, out_features), torch.float16, X.device, stream)
     _check("paro_linear_once", lib().paro_linear_once(
         x, pairs.ctypes.data if K else None, theta.ctypes.data if K else None,
-        alpha.ctypes.data, _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"),
-        _dev(zp, torch.uint8, "zeros"), _dev(Y, torch.float16, "Y"), T, in_f, out_features, K, P,
+        alpha.ctypes.data, *_weights(qw, sp, zp, in_f, out_features, 128, X.get_device()),
+        _dev(Y, torch.float16, "Y"), T, in_f, out_features, K, P,
         _stream(stream, X.device)))
     return Y
 
@@ -356,7 +389,7 @@ def paro_linear_ex(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fea
         b = _dev(bias, torch.float16, "bias")
     _check("paro_linear_ex", lib().paro_linear_ex(
         rot.handle if rot is not None else None, x,
-        _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, group,
+        *_weights(qw, sp, zp, in_f, out_features, group, X.get_device()), b, group,
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
     return Y
@@ -379,7 +412,7 @@ def _bias(bias: Optional[torch.Tensor], n: int) -> Optional[int]:
 def _same_device(X: torch.Tensor, **others) -> None:
     for name, t in others.items():
         if t is not None and t.device != X.device:
-            raise ValueError(f"{name} is on {t.device}, X on {X.device}")
+            raise ValueError(f"{name} is on {t.device}, not on {X.device}")
 
 
 def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_features: int, act: str = "none",
@@ -388,8 +421,9 @@ def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fe
     """Y = act((X T^-1) w_hat^T + bias) + residual, rounded once; Y may be the residual."""
     a, b = _act(act), _bias(bias, out_features)
     x = _dev(X, torch.float16, "X")
-    _same_device(X, qweight=qw, scales=sp, zeros=zp, bias=bias, workspace=ws)
+    _same_device(X, bias=bias, workspace=ws)
     T, in_f = X.shape
+    w = _weights(qw, sp, zp, in_f, out_features, group, X.get_device())
     shape = (T, out_features)
     r = None if residual is None else _f16(residual, shape, X.get_device(), "residual")
     Y = _out(Y, shape, torch.float16, X.device, "Y", stream)
@@ -397,9 +431,8 @@ def paro_linear_act(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, out_fe
         ws = _scratch(T, in_f, out_features, X.device, stream)
     with _on(X.device):
         _check("paro_linear_act", lib().paro_linear_act(
-            rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
-            _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, r, a, group, Y.data_ptr(), T, in_f,
-            out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
+            rot.handle if rot is not None else None, x, *w, b, r, a, group, Y.data_ptr(), T, in_f, out_features,
+            _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
     return Y
 
 
@@ -410,15 +443,15 @@ def paro_pack_gated(q: torch.Tensor, s: torch.Tensor, z: torch.Tensor, stream=No
     out_f, in_f = q.shape
     if out_f % 2:
         raise ValueError("q must hold as many up rows as gate rows")
-    if s.shape != (out_f, in_f // group) or z.shape != s.shape:
+    if group > 0 and (s.shape != (out_f, in_f // group) or z.shape != s.shape):
         raise ValueError("s and z must be [2 inter][in/group]")
-    qb, sb, zb = paro_pack_size(in_f, out_f, group)
+    sizes = paro_pack_size(in_f, out_f, group)
     dev = device or (q.device if q.is_cuda else torch.device("cuda", torch.cuda.current_device()))
-    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in (qb, sb, zb))
+    qw, sp, zp = (_empty(n, torch.uint8, dev, stream) for n in sizes)
+    logical = _logical(q, s, z, group, qw.device)
     with _on(qw.device):
         _check("paro_pack_gated", lib().paro_pack_gated(
-            _any(q, torch.uint8, "q"), _any(s, torch.float16, "s"), _any(z, torch.uint8, "z"), in_f, out_f // 2, group,
-            qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
+            *logical, in_f, out_f // 2, group, qw.data_ptr(), sp.data_ptr(), zp.data_ptr(), _stream(stream, qw.device)))
     return qw, sp, zp
 
 
@@ -429,16 +462,16 @@ def paro_linear_gated(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, inte
     from paro_pack_gated, bias [2 inter] (the gate's first)."""
     a, b = _act(act), _bias(bias, 2 * inter_features)
     x = _dev(X, torch.float16, "X")
-    _same_device(X, qweight=qw, scales=sp, zeros=zp, bias=bias, workspace=ws)
+    _same_device(X, bias=bias, workspace=ws)
     T, in_f = X.shape
+    w = _weights(qw, sp, zp, in_f, 2 * inter_features, group, X.get_device())
     H = _out(H, (T, inter_features), torch.float16, X.device, "H", stream)
     if ws is None:
         ws = _scratch(T, in_f, 2 * inter_features, X.device, stream)
     with _on(X.device):
         _check("paro_linear_gated", lib().paro_linear_gated(
-            rot.handle if rot is not None else None, x, _dev(qw, torch.uint8, "qweight"),
-            _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), b, a, group, H.data_ptr(), T, in_f,
-            inter_features, _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
+            rot.handle if rot is not None else None, x, *w, b, a, group, H.data_ptr(), T, in_f, inter_features,
+            _dev(ws, torch.uint8, "workspace"), ws.numel(), _stream(stream, X.device)))
     return H
 
 
@@ -466,15 +499,15 @@ class ParoLinear:
         self._a = _act(act)
         self._tensors = (qw, sp, zp, bias)                 # kept alive for the pointers below
         self._h = rot.handle if rot is not None else None
-        self._qw, self._sp, self._zp = _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), \
-            _dev(zp, torch.uint8, "zeros")
         rows = self._width_factor * self.out_features
-        for t, need in zip((qw, sp, zp), paro_pack_size(self.in_features, rows, group)):
-            if t.numel() < need:
-                raise ValueError(f"packed weights of {t.numel()} bytes, {need} needed for this shape and group")
-        self._b = _bias(bias, rows)
-        self.device = qw.device if device is None else torch.device(device)
+        _dev(qw, torch.uint8, "qweight")
         self._index = qw.get_device()
+        self._qw, self._sp, self._zp = _weights(qw, sp, zp, self.in_features, rows, group, self._index)
+        self._b = _bias(bias, rows)
+        _same_device(qw, bias=bias)
+        self.device = qw.device
+        if device is not None and torch.empty(0, device=device).device != self.device:
+            raise ValueError(f"the layer is on {self.device}, where its weights are, not on {device}")
         self._ws = None
         self._kept = []                                    # outgrown workspaces
         self._ws_tokens = 0
@@ -563,7 +596,7 @@ def paro_linear_partial(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
         ws = _scratch(T, in_f, out_features, X.device, stream)
     _check("paro_linear_partial", lib().paro_linear_partial(
         rot.handle if rot is not None else None, x,
-        _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"), group,
+        *_weights(qw, sp, zp, in_f, out_features, group, X.get_device()), group,
         _dev(Yf, torch.float32, "Yf"), T, in_f, out_features, _dev(ws, torch.uint8, "workspace"), ws.numel(),
         _stream(stream, X.device)))
     return Yf
@@ -592,7 +625,7 @@ def paro_linear_noalloc(rot: Optional[Rotation], X: torch.Tensor, qw, sp, zp, ou
         Y = _empty((T, out_features), torch.float16, X.device, stream)
     _check("paro_linear_noalloc", lib().paro_linear_noalloc(
         rot.handle if rot is not None else None, x,
-        _dev(qw, torch.uint8, "qweight"), _dev(sp, torch.uint8, "scales"), _dev(zp, torch.uint8, "zeros"),
+        *_weights(qw, sp, zp, in_f, out_features, 128, X.get_device()),
         _dev(Y, torch.float16, "Y"), T, in_f, out_features, _stream(stream, X.device)))
     return Y
 
