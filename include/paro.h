@@ -223,7 +223,7 @@ typedef enum {
  *                 may be Y_dev itself (Y += layer(X) in place)
  *   act           a paro_act
  * Y may share memory with the residual only, and only as the same pointer;
- * the workspace shares none with X, the residual or Y (else PARO_ERR_ARG).
+ * the workspace shares none with an input or Y (else PARO_ERR_ARG).
  * Other arguments, workspace and errors as paro_linear_ex. Above 16 tokens
  * the product runs on pairs of SMs (tcgen05 with cta_group::2). The result
  * has the same bits in every call with the same arguments. A rotation handle

@@ -668,12 +668,17 @@ paro_status linear_impl(const paro_rot* r, const void* X, const void* qw, const 
         const size_t nx = (size_t)T * in * 2, ny = (size_t)T * (epi.kind == paro::kEpiGated ? out / 2 : out) * 2;
         const void* R = epi.residual;
         if (!aligned16(R)) return fail(PARO_ERR_ARG, "pointers must be 16-byte aligned");
-        if (overlap(Y, ny, X, nx) || overlap(Y, ny, ws, need) || overlap(Y, ny, bias, (size_t)out * 2) ||
-            overlap(Y, ny, qw, (size_t)in * out / 2))
-            return fail(PARO_ERR_ARG, "the output overlaps an input or the workspace");
+        size_t nqw = 0, nsp = 0, nzp = 0;
+        paro_pack_size_ex(in, out, group, &nqw, &nsp, &nzp);
+        const struct { const void* p; size_t bytes; } inputs[] = {
+            {X, nx}, {bias, (size_t)out * 2}, {qw, nqw}, {sp, nsp}, {zp, nzp}};
+        if (overlap(Y, ny, ws, need)) return fail(PARO_ERR_ARG, "the output overlaps an input or the workspace");
+        for (const auto& v : inputs)
+            if (overlap(Y, ny, v.p, v.bytes)) return fail(PARO_ERR_ARG, "the output overlaps an input or the workspace");
         if (R != Y && overlap(R, ny, Y, ny)) return fail(PARO_ERR_ARG, "residual and output overlap without being the same");
-        if (overlap(ws, need, X, nx) || overlap(ws, need, R, ny) || overlap(ws, need, bias, (size_t)out * 2))
-            return fail(PARO_ERR_ARG, "the workspace overlaps an input");
+        bool shared = overlap(ws, need, R, ny);
+        for (const auto& v : inputs) shared = shared || overlap(ws, need, v.p, v.bytes);
+        if (shared) return fail(PARO_ERR_ARG, "the workspace overlaps an input");
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const paro::RotDev* rd = r ? &r->dev : nullptr;
