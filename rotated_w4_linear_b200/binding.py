@@ -112,6 +112,17 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+def _capturing(stream, device: torch.device) -> bool:
+    """Whether a CUDA graph is being captured on the stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return _is_capturing()
+
+
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -481,11 +492,12 @@ class ParoLinear:
     here; a call checks only X, Y and the residual and hands raw pointers to
     the same C entry points as paro_linear_ex and paro_linear_act (the latter
     with an activation or a residual). The workspace is owned by the object
-    and grows with the largest batch seen (at least twofold; outgrown ones are
-    kept, since a captured CUDA graph goes on using the one of its time), so
-    calls on one object must not overlap on the GPU (one stream, or events),
-    as for paro_linear's workspace, and the object must outlive the graphs
-    that captured it. The object keeps references to the tensors it was
+    and has the size of the largest batch seen; an outgrown one is kept if it
+    may still be used, by a CUDA graph that captured a call or by a call on
+    another stream than the one whose memory it is. So calls on one object must
+    not overlap on the GPU (one stream, or events), as for paro_linear's
+    workspace, and the object must outlive the graphs that captured it and its
+    calls on other streams. The object keeps references to the tensors it was
     given."""
 
     _width_factor = 1                                   # rows of the weights per output column
@@ -509,18 +521,20 @@ class ParoLinear:
         if device is not None and torch.empty(0, device=device).device != self.device:
             raise ValueError(f"the layer is on {self.device}, where its weights are, not on {device}")
         self._ws = None
-        self._kept = []                                    # outgrown workspaces
         self._ws_tokens = 0
+        self._ws_stream = None                             # raw stream whose memory the workspace is
+        self._ws_shared = False                            # a graph or another stream may use it
+        self._kept = []                                    # outgrown workspaces that were shared
         self._f = lib().paro_linear_ex
         self._f_act = lib().paro_linear_act
 
     def _workspace(self, T: int, stream=None) -> None:
         if T > self._ws_tokens or self._ws is None:
-            if self._ws is not None:
+            if self._ws_shared:
                 self._kept.append(self._ws)
-            tokens = max(T, 2 * self._ws_tokens)
-            self._ws = _scratch(tokens, self.in_features, self._width_factor * self.out_features, self.device, stream)
-            self._ws_tokens = tokens
+            self._ws = None                                # its memory may serve the next one
+            self._ws = _scratch(T, self.in_features, self._width_factor * self.out_features, self.device, stream)
+            self._ws_tokens, self._ws_stream, self._ws_shared = T, _stream(stream, self.device), False
 
     def _prepare(self, X, Y, stream):
         """(tokens, Y, raw stream) of a call, after its checks."""
@@ -536,9 +550,15 @@ class ParoLinear:
             raise ValueError(f"X on {X.device}, Y on {Y.device}, the layer on {self.device}")
         if T > self._ws_tokens or self._ws is None:
             self._workspace(T, stream)
-        if stream is None:
-            return T, Y, int(_raw_stream(X.get_device())) if _raw_stream is not None else _stream(None, X.device)
-        return T, Y, _stream(stream, X.device)
+        if stream is None and _raw_stream is not None:
+            raw = int(_raw_stream(X.get_device()))
+        else:
+            raw = _stream(stream, X.device)
+        # (the default stream, raw 0, cannot be captured; asking costs 0.3 us)
+        if not self._ws_shared and (raw != self._ws_stream or raw != 0 and
+                                    (_is_capturing() if stream is None else _capturing(stream, X.device))):
+            self._ws_shared = True
+        return T, Y, raw
 
     def __call__(self, X: torch.Tensor, Y: Optional[torch.Tensor] = None, stream=None,
                  residual: Optional[torch.Tensor] = None) -> torch.Tensor:
