@@ -222,14 +222,17 @@ def _weights(qw, sp, zp, in_features: int, rows: int, group: int, device: int):
     """Data pointers of packed weights, which must hold `rows` output rows of
     in_features channels in groups of `group` and lie on CUDA device `device`:
     the kernels read that much from there."""
-    ptrs = []
-    for name, t, need in zip(("qweight", "scales", "zeros"), (qw, sp, zp), _packed_bytes(in_features, rows, group)):
-        ptrs.append(_dev(t, torch.uint8, name))
-        if t.numel() < need:
-            raise ValueError(f"{name} holds {t.numel()} bytes, {need} needed for {rows} x {in_features} in groups of {group}")
+    need = _packed_bytes(in_features, rows, group)
+    for name, t, n in zip(("qweight", "scales", "zeros"), (qw, sp, zp), need):
+        if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.get_device() == device >= 0 \
+                and t.numel() >= n and t.is_contiguous():
+            continue
+        _dev(t, torch.uint8, name)                          # says what is wrong, if not the size or the place
+        if t.numel() < n:
+            raise ValueError(f"{name} holds {t.numel()} bytes, {n} needed for {rows} x {in_features} in groups of {group}")
         if t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, not on CUDA device {device}")
-    return ptrs
+    return qw.data_ptr(), sp.data_ptr(), zp.data_ptr()
 
 
 def _any(t, dtype, name) -> int:

@@ -129,3 +129,16 @@ def test_packs(B, pack):
             call(*logical(**{name: away}), device=torch.device("cuda", 0))
     with pytest.raises(B.ParoError):
         call(*logical(), group=0)
+
+
+def test_host_weights_never_reach_the_library(monkeypatch):
+    """The same calls on host tensors, with the real type checks."""
+    from rotated_w4_linear_b200 import binding
+    w = [torch.zeros(n, dtype=torch.uint8) for n in binding.paro_pack_size(N_IN, N_OUT, 128)]
+    monkeypatch.setattr(binding, "_check", lambda *args: pytest.fail("the library was reached"))
+    x = torch.zeros(4, N_IN, dtype=torch.float16)
+    for call in (lambda: binding.paro_dequant(*w, N_IN, N_OUT), lambda: binding.paro_linear_act(None, x, *w, N_OUT),
+                 lambda: binding.paro_linear_ex(None, x, *w, N_OUT), lambda: binding.ParoLinear(None, *w, N_IN, N_OUT),
+                 lambda: binding.paro_dequant(None, *w[1:], N_IN, N_OUT)):
+        with pytest.raises((TypeError, AttributeError)):
+            call()
