@@ -60,6 +60,7 @@
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
+#include "pair_plan.h"
 #include "sm100.cuh"
 
 namespace paro {
@@ -103,8 +104,6 @@ struct PairCfg {
     static_assert(BN + 64 * kXStages <= 512, "tensor memory");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
-constexpr int kMaxPairs = 4;                            // pairs that may split a tile's channels (cluster of 8)
-
 struct PairArgs {
     int T, out, nk;             // nk: 128-channel stages
     int mt, ntiles;             // 256-row tiles; tiles in all
@@ -765,45 +764,6 @@ cudaError_t pair_clusters(int dev, int pairs, int* clusters) {
     return cudaSuccess;
 }
 
-// Tokens of a tile of the 256-token form: the batch in as few tiles as it
-// takes, of equal size in steps of 32 (333 tokens: two tiles of 192, not of 256).
-int balanced_tile(int T) {
-    const int tiles = (T + 255) / 256;
-    return (((T + tiles - 1) / tiles) + 31) / 32 * 32;
-}
-
-// What a product takes in each form, in SM cycles: rounds of tiles that do not
-// fit at once, times a tile's stages and its start and end. The figures are
-// measured (4096 -> 28672 and 14336 -> 4096, 17 to 512 tokens): a stage of the
-// 256-token form 1250 (less for smaller tiles, down to the dequantisation's
-// 900) and a tile's change-over 4000; a stage of the split form
-// 800, its start, exchange and end 11000, 1500 more with several pairs. Taking
-// the cheaper one, 4096 -> 4096 at 256 tokens runs in the split form (32 tiles
-// of 128 tokens, two pairs each) and 4096 -> 28672 at 256 in the other.
-struct PairPlan {
-    long cost = 0;
-    int pairs = 1;
-};
-template <int BN, int EPI>
-cudaError_t plan_pair(int dev, const PairArgs& a, PairPlan* plan) {
-    const int bn = PairCfg<BN>::kSplit ? BN : balanced_tile(a.T);
-    const int tiles = a.mt * ((a.T + bn - 1) / bn);
-    *plan = PairPlan();
-    for (int p = 1; p <= (PairCfg<BN>::kSplit ? std::min(kMaxPairs, a.nk) : 1); ++p) {
-        int n = 0;
-        const cudaError_t e = pair_clusters<BN, EPI>(dev, p, &n);
-        if (e != cudaSuccess) return e;
-        const long rounds = (tiles + n - 1) / n, stages = (a.nk + p - 1) / p;
-        const long cost = PairCfg<BN>::kSplit ? rounds * (stages * 800 + 11000 + (p > 1 ? 1500 : 0))
-                                              : rounds * (stages * std::max(900, 1250 * bn / 256) + 4000) + 6000;
-        if (plan->cost == 0 || cost < plan->cost) {
-            plan->cost = cost;
-            plan->pairs = p;
-        }
-    }
-    return cudaSuccess;
-}
-
 template <int BN, int EPI>
 cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPlan& plan, cudaStream_t s) {
     a.ntiles = a.mt * ((a.T + a.bn - 1) / a.bn);
@@ -842,7 +802,7 @@ cudaError_t launch_pair(int dev, const CUtensorMap* tm, PairArgs a, const PairPl
 template <int BN, int EPI>
 cudaError_t encode_and_launch(int dev, const void* Xr, const void* qw, const void* scp, const void* zp, int64_t in,
                               int group, PairArgs a, const PairPlan& plan, cudaStream_t s) {
-    a.bn = PairCfg<BN>::kSplit ? BN : balanced_tile(a.T);
+    a.bn = plan.bn;
     const uint64_t G = (uint64_t)(in / group), Gp = G + (G & 1), nrb = (uint64_t)(a.out / 16);
     const uint32_t cols = EPI == kEpiGated ? 16u : 32u;
     CUtensorMap tm[6];
@@ -861,25 +821,24 @@ cudaError_t encode_and_launch(int dev, const void* Xr, const void* qw, const voi
     return ok ? launch_pair<BN, EPI>(dev, tm, a, plan, s) : cudaErrorInvalidValue;
 }
 
-// 17 to 64 tokens: tiles of 64; to 128: tiles of 128; above: the cheaper of
-// the split form with tiles of 128 and the persistent one with tiles of 256.
 template <int EPI>
 cudaError_t plan_and_launch(const void* Xr, const void* qw, const void* scp, const void* zp, int64_t in, int group,
                             const PairArgs& a, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    PairPlan split, whole;
-    if (a.T <= 64) {
-        e = plan_pair<64, EPI>(dev, a, &split);
-        return e != cudaSuccess ? e : encode_and_launch<64, EPI>(dev, Xr, qw, scp, zp, in, group, a, split, s);
-    }
-    e = plan_pair<128, EPI>(dev, a, &split);
-    if (e == cudaSuccess && a.T > 128) e = plan_pair<256, EPI>(dev, a, &whole);
+    const PairPlan plan = plan_pairs(a.mt, a.T, a.nk, [&](int form, int pairs) {
+        int n = 0;
+        const cudaError_t err = form == 64    ? pair_clusters<64, EPI>(dev, pairs, &n)
+                                : form == 128 ? pair_clusters<128, EPI>(dev, pairs, &n)
+                                              : pair_clusters<256, EPI>(dev, pairs, &n);
+        if (err != cudaSuccess) e = err;
+        return err == cudaSuccess ? n : 0;
+    });
     if (e != cudaSuccess) return e;
-    return a.T <= 128 || split.cost < whole.cost
-               ? encode_and_launch<128, EPI>(dev, Xr, qw, scp, zp, in, group, a, split, s)
-               : encode_and_launch<256, EPI>(dev, Xr, qw, scp, zp, in, group, a, whole, s);
+    return plan.form == 64    ? encode_and_launch<64, EPI>(dev, Xr, qw, scp, zp, in, group, a, plan, s)
+           : plan.form == 128 ? encode_and_launch<128, EPI>(dev, Xr, qw, scp, zp, in, group, a, plan, s)
+                              : encode_and_launch<256, EPI>(dev, Xr, qw, scp, zp, in, group, a, plan, s);
 }
 
 }  // namespace
