@@ -27,6 +27,11 @@
  *     synchronising; the stream is a cudaStream_t (0 = legacy default stream).
  *     Hot-path calls (paro_rotate, paro_linear) allocate nothing.
  *   - Device pointers must be 16-byte aligned.
+ *   - Layer calls are programmatic dependent launches: decode batches begin to
+ *     read the packed weights while the kernel enqueued just before them still
+ *     runs (everything else waits for it). Packing calls take care of this;
+ *     weights that a kernel of the caller's own writes need some other
+ *     operation on the stream between it and the layer call.
  *   - Every call returns a paro_status; on anything but PARO_OK,
  *     paro_last_error() returns a message for the calling thread. Argument
  *     errors are detected on the host before anything is enqueued.

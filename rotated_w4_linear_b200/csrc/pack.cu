@@ -64,6 +64,11 @@ __global__ void pack_meta_kernel(const uint16_t* __restrict__ s, const uint8_t* 
     if ((G & 1) && gi == G - 1) zp[(rb * Gp + G) * 8 + g] = 0;   // padding group
 }
 
+// Launched in order after the packs: a decode call enqueued next streams weights
+// before the grid just before it is complete (programmatic dependent launch),
+// which is then this one, and the packed weights are complete and visible.
+__global__ void pack_done_kernel() {}
+
 cudaError_t launch_pack(const uint8_t* q, const uint16_t* sc, const uint8_t* z, int64_t in, int64_t out, int group,
                         void* qw, void* scp, void* zp, cudaStream_t s, bool gated) {
     const int inter = gated ? (int)(out / 2) : 0;
@@ -76,6 +81,7 @@ cudaError_t launch_pack(const uint8_t* q, const uint16_t* sc, const uint8_t* z, 
     if (nm > 0)
         pack_meta_kernel<<<(unsigned)((nm + 255) / 256), 256, 0, s>>>(sc, z, static_cast<uint32_t*>(scp),
                                                                       static_cast<uint8_t*>(zp), G, rep, inter, nm);
+    pack_done_kernel<<<1, 1, 0, s>>>();
     return cudaGetLastError();
 }
 
