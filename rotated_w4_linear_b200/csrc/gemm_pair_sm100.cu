@@ -46,8 +46,8 @@
 // with the MMAs issued from a converged warp; loads issued the same way and
 // the dequantisation in groups of four warps took another 12% off the time,
 // which is then the power limit's: 1455 us for 4096 -> 2 x 14336 at 8192 tokens
-// (1320 TFLOP/s at 1.2-1.35 GHz), 341 us and the tensor pipe 85% busy at 2048.
-// BN = 64: 14336 -> 4096 at 64 tokens 19.8 us (one CTA per tile, unsplit: 94).
+// (1320 TFLOP/s at 1.2-1.35 GHz), 339 us and the tensor pipe 86% busy at 2048.
+// BN = 64: 14336 -> 4096 at 64 tokens 19.8-20.2 us (one CTA per tile, unsplit: 94).
 //
 // A token's result does not depend on its place in the batch: the order of the
 // channels goes by the row tile and the split alone.
