@@ -222,9 +222,9 @@ typedef enum {
  * with the bias, the activation and the residual applied to the fp32 sum
  * before the single rounding to fp16. The operand X T^-1 is the fp16 one that
  * paro_rotate returns (the tensor cores' type), in this call and the gated one
- * as in paro_linear: each channel rounded by at most 2^-11 of its value. (The paper's layer is act none and R
- * zero; a decoder block adds its attention output and down projections to
- * the residual stream this way.)
+ * as in paro_linear: each channel rounded by at most 2^-11 of its value. (The
+ * paper's layer is act none and R zero; a decoder block adds its attention
+ * output and down projections to the residual stream this way.)
  *   bias_dev      fp16 [out_features] or NULL
  *   residual_dev  R, fp16 [tokens][out_features] (16-byte aligned) or NULL; it
  *                 may be Y_dev itself (Y += layer(X) in place)
